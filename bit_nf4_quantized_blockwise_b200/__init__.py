@@ -26,5 +26,6 @@ from ._lib import (  # noqa: F401
     qlora_quantize_nf4,
     quantize_weight,
 )
+from .multi_adamw import MultiAdamW  # noqa: F401
 
 __version__ = "1.0.0"

@@ -34,6 +34,17 @@ class qlora_adamw_t(ctypes.Structure):
                 ("weight_decay", _c_float), ("max_grad_norm", _c_float), ("step", ctypes.c_int32)]
 
 
+class qlora_adamw_tensor_t(ctypes.Structure):
+    """Mirror of the C struct qlora_adamw_tensor_t."""
+    _fields_ = [("param", _c_void_p), ("copy", _c_void_p), ("n", _c_i64)]
+
+
+class qlora_adamw_state_t(ctypes.Structure):
+    """Mirror of the C struct qlora_adamw_state_t."""
+    _fields_ = [("m", _c_void_p), ("v", _c_void_p), ("m_scale", _c_void_p), ("v_scale", _c_void_p),
+                ("steps", _c_void_p), ("bits", ctypes.c_int32)]
+
+
 class qlora_nf4_t(ctypes.Structure):
     """Mirror of the C struct qlora_nf4_t."""
     _fields_ = [
@@ -84,6 +95,11 @@ EXPORTS = {
     "qlora_grad_sqnorm": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p]),
     "qlora_adamw_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_i64, _c_void_p,
                                   _c_void_p, _c_void_p]),
+    "qlora_multi_adamw_state_elems": (_c_i64, [_c_void_p, _c_int]),
+    "qlora_multi_adamw_plan_size": (_c_size, [_c_int]),
+    "qlora_multi_adamw_plan": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "qlora_multi_adamw_step": (_c_int, [_c_void_p, _c_size, _c_int, _c_i64, _c_void_p, _c_int, _c_void_p, _c_void_p,
+                                        _c_void_p]),
     "qlora_check_status": (_c_int, [_c_void_p]),
     "qlora_debug_wait_tags": (ctypes.c_uint, []),
     "qlora_debug_wait_probe": (_c_int, [ctypes.c_uint64, _c_void_p]),

@@ -86,4 +86,358 @@ __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const
   }
 }
 
+// ====================================================================== AdamW over many tensors
+
+// One AdamW step over a list of tensors (the L1, L2 factors of every linear),
+// in two launches whatever their number: multi_adamw_prepare_kernel sums the
+// squares of all gradients and turns the step counts and the norm into
+// coefficients, multi_adamw_kernel updates every element once.
+//
+// The state is one flat array per moment in which each tensor starts a new
+// block of MA_BLOCK = 256 elements (a warp's work, 8 elements a lane).
+//   32 bits: m and v in fp32.
+//   8 bits:  m and r = sqrt(v) as FP8 E4M3 codes, and one fp32 scale
+//     c = max|x| / 448 per block: the value of a code e is E4M3(e) c, the code of
+//     x is E4M3(x 448 / max|x|) (round to nearest even), the rule the block
+//     constants of the weights are stored by.  r and not v is stored, because
+//     the root spans half the binades: E4M3 reaches 2^-17.8 of the block's
+//     largest value, which is 2^-35.6 of the largest v, and a v that fell to 0
+//     would divide m by eps alone.  A positive r that rounds to 0 takes the
+//     smallest code, 2^-9, for the same reason.  The step itself uses the fp32
+//     m and r from before they are rounded to codes.
+// Bytes a parameter: 8 (param) + 4 or 2 (gradient) + 2 (copy) + 16 or 4.06
+// (state), and the gradient once more for the norm.
+constexpr int MA_BLOCK = 256;
+constexpr int MA_THREADS = 256;
+constexpr int MA_WARPS = MA_THREADS / 32;
+constexpr int MA_PTRS = 496;          // gradient pointers passed with a launch (under 4 KB of parameters)
+constexpr int MA_NORM_CTAS = 148 * 4; // partial sums of the norm, one per CTA
+
+struct MultiTensor {
+  float* p;         // fp32 [n]
+  uint16_t* copy;   // bf16 [n], or null
+  int64_t n;
+  int64_t block0;   // first block of the tensor in the flat state
+};
+
+struct MultiCoef {
+  float step_size;  // lr / (1 - beta1^t), t the tensor's own step count
+  float bc2_sqrt;   // sqrt(1 - beta2^t)
+};
+
+// Device side of a plan, in this order in one allocation.
+struct MultiHead {
+  double partial[MA_NORM_CTAS];
+  unsigned ticket;  // CTAs of the norm done, back at 0 after every launch
+  float clip;
+  int64_t blocks;
+};
+
+struct MultiAdamWParams {
+  MultiHead* head;
+  MultiTensor* tensors;   // [count + 1]; the last one only closes block0
+  MultiCoef* coef;        // [count]
+  const void** stored;    // gradient pointers in memory (lists longer than MA_PTRS)
+  int count;
+  int from_memory;
+  void* m;                // flat state, fp32 or E4M3
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int32_t* steps;         // [count] completed steps of each tensor
+  float lr, beta1, beta2, eps, weight_decay, max_grad_norm;
+  int clip;               // clip by the global norm
+};
+
+struct GradPtrs {
+  const void* g[MA_PTRS];
+};
+
+// Copies gradient pointers first .. first + n - 1 of a long list into the plan.
+__global__ void __launch_bounds__(128) multi_adamw_ptrs_kernel(const __grid_constant__ GradPtrs gp, const void** dst,
+                                                               int n) {
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) dst[i] = gp.g[i];
+}
+
+__device__ __forceinline__ const void* multi_grad(const MultiAdamWParams& a, const GradPtrs& gp, int t) {
+  return a.from_memory ? a.stored[t] : gp.g[t];
+}
+
+// The tensor that holds block b: the last one with block0 <= b.
+__device__ __forceinline__ int multi_find(const MultiTensor* ts, int count, int64_t b) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ts[mid].block0 <= b)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// A lane's 8 elements of a block: 4 lane .. 4 lane + 3 and 128 more.
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, int left, bool vec, int lane, float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 128 * h + 4 * lane;
+    if (vec && i + 4 <= left) {
+      if constexpr (sizeof(T) == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src + i);
+        x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
+      } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(src + i);
+        x[4 * h] = __uint_as_float(u.x << 16), x[4 * h + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+        x[4 * h + 2] = __uint_as_float(u.y << 16), x[4 * h + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4)
+          x[4 * h + j] = i + j < left ? static_cast<float>(src[i + j]) : 0.0f;
+        else
+          x[4 * h + j] = i + j < left ? bf16_bits_to_float(src[i + j]) : 0.0f;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(float* dst, int left, bool vec, int lane, const float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 128 * h + 4 * lane;
+    if (vec && i + 4 <= left) {
+      *reinterpret_cast<float4*>(dst + i) = make_float4(x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < left) dst[i + j] = x[4 * h + j];
+    }
+  }
+}
+
+__device__ __forceinline__ bool vec_ok(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
+// The norm of all gradients (fp64; the partial sums of the CTAs are added in
+// order, so the norm does not depend on timing) and, in the CTA that ends
+// last, the clipping factor and each tensor's coefficients.  A tensor without
+// gradient (null pointer) is left out and its step count stands.
+template <typename G>
+__global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const __grid_constant__ MultiAdamWParams a,
+                                                                         const __grid_constant__ GradPtrs gp) {
+  __shared__ double part[MA_WARPS];
+  __shared__ bool last;
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  double s = 0.0;
+  if (a.clip) {
+    const int64_t blocks = a.head->blocks;
+    const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+    int t = -1;
+    int64_t next = 0, first = 0, n = 0;
+    const G* g = nullptr;
+    bool vec = false;
+    for (int64_t b = b0 + warp; b < b1; b += MA_WARPS) {
+      if (t < 0 || b >= next) {
+        t = t < 0 ? multi_find(a.tensors, a.count, b) : t + 1;
+        while (a.tensors[t + 1].block0 <= b) ++t;
+        first = a.tensors[t].block0;
+        next = a.tensors[t + 1].block0;
+        n = a.tensors[t].n;
+        g = static_cast<const G*>(multi_grad(a, gp, t));
+        vec = vec_ok(g, 4 * sizeof(G));
+      }
+      if (!g) continue;
+      const int64_t e = (b - first) * MA_BLOCK;
+      const int left = static_cast<int>(n - e < MA_BLOCK ? n - e : MA_BLOCK);
+      float x[8];
+      load8<G>(g + e, left, vec, lane, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += static_cast<double>(x[j]) * x[j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) part[warp] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double x = 0.0;
+    for (int i = 0; i < MA_WARPS; ++i) x += part[i];
+    a.head->partial[blockIdx.x] = x;
+    __threadfence();
+    last = atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int t = threadIdx.x; t < a.count; t += MA_THREADS) {
+    if (!multi_grad(a, gp, t)) continue;
+    const int k = ++a.steps[t];
+    MultiCoef c;
+    c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k)));
+    c.bc2_sqrt = static_cast<float>(sqrt(1.0 - pow(static_cast<double>(a.beta2), k)));
+    a.coef[t] = c;
+  }
+  if (warp == 0) {
+    double x = 0.0;
+    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) x += __ldcg(a.head->partial + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    if (lane == 0) {
+      const float c = static_cast<float>(static_cast<double>(a.max_grad_norm) / (sqrt(x) + 1e-6));
+      a.head->clip = a.clip && c < 1.0f ? c : 1.0f;
+      a.head->ticket = 0;
+    }
+  }
+}
+
+// E4M3 codes of a lane's 8 values of a block under inv = 448 / max, and back.
+template <bool kRoot>
+__device__ __forceinline__ uint2 state_encode(const float (&x)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      y[j] = __fmul_rn(x[4 * h + j], inv);
+      if (kRoot && y[j] > 0.0f && y[j] < 0x1p-9f) y[j] = 0x1p-9f;  // above 0 stays above 0
+    }
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    w[h] = lo | (hi << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void state_decode(uint2 w, float scale, float (&x)[8]) {
+  const uint32_t ws[2] = {w.x, w.y};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __half2 v = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(ws[h] >> (16 * j)), __NV_E4M3));
+      const float2 f = __half22float2(v);
+      x[4 * h + 2 * j] = __fmul_rn(f.x, scale);
+      x[4 * h + 2 * j + 1] = __fmul_rn(f.y, scale);
+    }
+}
+
+// The scale of a block and the factor of its codes, from the largest
+// magnitude's bits.  Blocks below 2^-100 (448 / max would overflow) hold zeros;
+// a NaN or an infinity makes the scale one of the two, so that its block
+// decodes to NaN.
+__device__ __forceinline__ void block_scale(uint32_t top_bits, float& scale, float& inv) {
+  const float top = __uint_as_float(top_bits);
+  const bool dead = top < 0x1p-100f;
+  scale = dead ? 0.0f : __fdiv_rn(top, 448.0f);
+  inv = dead ? 0.0f : __fdiv_rn(448.0f, top);
+}
+
+// The update, in adamw_kernel's order and rounding (fp32 IEEE throughout).  A
+// warp takes whole blocks of its CTA's contiguous range, from the end to the
+// beginning: the norm read the range upwards, so the gradients it read last
+// are still in L2.
+template <bool k8, typename G>
+__global__ void __launch_bounds__(MA_THREADS) multi_adamw_kernel(const __grid_constant__ MultiAdamWParams a,
+                                                                 const __grid_constant__ GradPtrs gp) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t blocks = a.head->blocks;
+  const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+  const float decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
+  const float one_m_b1 = __fsub_rn(1.0f, a.beta1), one_m_b2 = __fsub_rn(1.0f, a.beta2);
+  pdl_wait();  // coefficients, and the step before this one
+  const float clip = __ldcg(&a.head->clip);
+  int t = -1;
+  int64_t first = 0;
+  MultiTensor ts{};
+  MultiCoef c{};
+  const G* g = nullptr;
+  bool vec = false, gvec = false;
+  for (int64_t b = b1 - 1 - warp; b >= b0; b -= MA_WARPS) {
+    if (t < 0 || b < first) {
+      t = t < 0 ? multi_find(a.tensors, a.count, b) : t - 1;
+      while (a.tensors[t].block0 > b) --t;
+      ts = a.tensors[t];
+      first = ts.block0;
+      g = static_cast<const G*>(multi_grad(a, gp, t));
+      if (g) {
+        c.step_size = __ldcg(&a.coef[t].step_size);
+        c.bc2_sqrt = __ldcg(&a.coef[t].bc2_sqrt);
+      }
+      vec = vec_ok(ts.p, 16) && vec_ok(ts.copy, 8);
+      gvec = vec_ok(g, 4 * sizeof(G));
+    }
+    if (!g) continue;
+    const int64_t e = (b - first) * MA_BLOCK;
+    const int left = static_cast<int>(ts.n - e < MA_BLOCK ? ts.n - e : MA_BLOCK);
+    float p[8], x[8], m[8], v[8];
+    load8<G>(g + e, left, gvec, lane, x);
+    load8<float>(ts.p + e, left, vec, lane, p);
+    const int64_t at = b * MA_BLOCK + 4 * lane;  // the flat state is padded to whole blocks
+    if constexpr (k8) {
+      const uint8_t* mc = static_cast<const uint8_t*>(a.m) + at;
+      const uint8_t* vc = static_cast<const uint8_t*>(a.v) + at;
+      const uint2 mw = make_uint2(*reinterpret_cast<const uint32_t*>(mc), *reinterpret_cast<const uint32_t*>(mc + 128));
+      const uint2 vw = make_uint2(*reinterpret_cast<const uint32_t*>(vc), *reinterpret_cast<const uint32_t*>(vc + 128));
+      state_decode(mw, a.m_scale[b], m);
+      state_decode(vw, a.v_scale[b], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    } else {
+      load8<float>(static_cast<const float*>(a.m) + b * MA_BLOCK, MA_BLOCK, true, lane, m);
+      load8<float>(static_cast<const float*>(a.v) + b * MA_BLOCK, MA_BLOCK, true, lane, v);
+    }
+    float r[8];
+    uint32_t mtop = 0, rtop = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gi = __fmul_rn(x[j], clip);
+      m[j] = __fadd_rn(m[j], __fmul_rn(one_m_b1, __fsub_rn(gi, m[j])));
+      v[j] = __fadd_rn(__fmul_rn(a.beta2, v[j]), __fmul_rn(one_m_b2, __fmul_rn(gi, gi)));
+      r[j] = __fsqrt_rn(v[j]);
+      const float denom = __fadd_rn(__fdiv_rn(r[j], c.bc2_sqrt), a.eps);
+      p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(c.step_size, __fdiv_rn(m[j], denom)));
+      if constexpr (k8) {
+        // what lies behind the tensor's end does not count for the block
+        if (128 * (j >> 2) + 4 * lane + (j & 3) >= left) m[j] = r[j] = 0.0f;
+        mtop = max(mtop, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+        rtop = max(rtop, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+      }
+    }
+    store8(ts.p + e, left, vec, lane, p);
+    if (ts.copy) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 128 * h + 4 * lane;
+        const uint32_t w0 = pack_bf16x2(p[4 * h], p[4 * h + 1]), w1 = pack_bf16x2(p[4 * h + 2], p[4 * h + 3]);
+        if (vec && i + 4 <= left) {
+          *reinterpret_cast<uint2*>(ts.copy + e + i) = make_uint2(w0, w1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (i + j < left) ts.copy[e + i + j] = static_cast<uint16_t>((j < 2 ? w0 : w1) >> (16 * (j & 1)));
+        }
+      }
+    }
+    if constexpr (k8) {
+      float ms, minv, rs, rinv;
+      block_scale(__reduce_max_sync(0xFFFFFFFFu, mtop), ms, minv);
+      block_scale(__reduce_max_sync(0xFFFFFFFFu, rtop), rs, rinv);
+      const uint2 mw = state_encode<false>(m, minv), vw = state_encode<true>(r, rinv);
+      uint8_t* mc = static_cast<uint8_t*>(a.m) + at;
+      uint8_t* vc = static_cast<uint8_t*>(a.v) + at;
+      *reinterpret_cast<uint32_t*>(mc) = mw.x, *reinterpret_cast<uint32_t*>(mc + 128) = mw.y;
+      *reinterpret_cast<uint32_t*>(vc) = vw.x, *reinterpret_cast<uint32_t*>(vc + 128) = vw.y;
+      if (lane == 0) a.m_scale[b] = ms, a.v_scale[b] = rs;
+    } else {
+      store8(static_cast<float*>(a.m) + b * MA_BLOCK, left, true, lane, m);
+      store8(static_cast<float*>(a.v) + b * MA_BLOCK, left, true, lane, v);
+    }
+  }
+}
+
 }  // namespace qlora

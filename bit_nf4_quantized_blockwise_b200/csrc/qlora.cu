@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 using namespace qlora;
@@ -1181,6 +1182,180 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
                                                                                              param_bf16, n, a);
   }
   return launch_status();
+}
+
+}  // extern "C"
+
+namespace {
+
+// Where the parts of a many-tensor AdamW plan lie.
+struct MultiPlan {
+  MultiHead* head;
+  MultiTensor* tensors;
+  MultiCoef* coef;
+  const void** stored;
+  size_t bytes;
+};
+
+MultiPlan multi_plan_layout(void* base, int count) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* q = p ? p + off : nullptr;
+    off += round256(bytes);
+    return q;
+  };
+  MultiPlan m{};
+  m.head = static_cast<MultiHead*>(take(sizeof(MultiHead)));
+  m.tensors = static_cast<MultiTensor*>(take(sizeof(MultiTensor) * (static_cast<size_t>(count) + 1)));
+  m.coef = static_cast<MultiCoef*>(take(sizeof(MultiCoef) * static_cast<size_t>(count)));
+  m.stored = static_cast<const void**>(take(sizeof(void*) * static_cast<size_t>(count)));
+  m.bytes = off;
+  return m;
+}
+
+constexpr int kMaxTensors = 1 << 20;
+
+template <bool k8, typename G>
+int launch_multi_adamw(const MultiAdamWParams& a, const GradPtrs& gp, int64_t blocks, cudaStream_t st) {
+  const int64_t ctas = (blocks + MA_WARPS - 1) / MA_WARPS;
+  const int64_t norm = a.clip ? (ctas < MA_NORM_CTAS ? ctas : MA_NORM_CTAS) : 1;
+  {
+    LaunchScope ls(QLORA_KERNEL_OPTIM, st);
+    multi_adamw_prepare_kernel<G><<<static_cast<unsigned>(norm), MA_THREADS, 0, st>>>(a, gp);
+  }
+  if (launch_status() != QLORA_OK) return QLORA_ERR_CUDA;
+  const int64_t most = static_cast<int64_t>(sm_count()) * 4;
+  LaunchScope ls(QLORA_KERNEL_OPTIM, st);
+  // programmatic dependent launch: the update's blocks are set up while the norm is summed
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+  cfg.blockDim = dim3(MA_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, multi_adamw_kernel<k8, G>, a, gp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t qlora_multi_adamw_state_elems(const qlora_adamw_tensor_t* tensors, int count) {
+  if (!tensors || count < 1 || count > kMaxTensors) return 0;
+  int64_t blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    if (tensors[i].n < 1 || tensors[i].n > (int64_t(1) << 40)) return 0;
+    blocks += (tensors[i].n + MA_BLOCK - 1) / MA_BLOCK;
+  }
+  return blocks * MA_BLOCK;
+}
+
+size_t qlora_multi_adamw_plan_size(int count) {
+  return count < 1 || count > kMaxTensors ? 0 : multi_plan_layout(nullptr, count).bytes;
+}
+
+int qlora_multi_adamw_plan(const qlora_adamw_tensor_t* tensors, int count, void* plan, size_t plan_bytes,
+                           void* stream) {
+  if (!tensors) return QLORA_ERR_NULL;
+  if (count < 1 || count > kMaxTensors) return QLORA_ERR_SHAPE;
+  for (int i = 0; i < count; ++i) {
+    if (!tensors[i].param) return QLORA_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(tensors[i].param) & 3u) || (reinterpret_cast<uintptr_t>(tensors[i].copy) & 1u))
+      return QLORA_ERR_ALIGN;
+  }
+  const int64_t elems = qlora_multi_adamw_state_elems(tensors, count);
+  if (elems < 1) return QLORA_ERR_SHAPE;
+  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(plan)) return QLORA_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) return QLORA_ERR_UNSUPPORTED;  // a replay would read the host table again
+  MultiTensor* host = new (std::nothrow) MultiTensor[static_cast<size_t>(count) + 1];
+  MultiHead* head = new (std::nothrow) MultiHead();
+  int rc = host && head ? QLORA_OK : QLORA_ERR_WORKSPACE;
+  if (rc == QLORA_OK) {
+    const MultiPlan mp = multi_plan_layout(plan, count);
+    int64_t b = 0;
+    for (int i = 0; i < count; ++i) {
+      host[i] = {tensors[i].param, tensors[i].copy, tensors[i].n, b};
+      b += (tensors[i].n + MA_BLOCK - 1) / MA_BLOCK;
+    }
+    host[count] = {nullptr, nullptr, 0, b};
+    head->blocks = b;
+    // both copies are from pageable memory, which the calls have read when they return
+    if (cudaMemcpyAsync(mp.head, head, sizeof(MultiHead), cudaMemcpyHostToDevice, st) != cudaSuccess ||
+        cudaMemcpyAsync(mp.tensors, host, sizeof(MultiTensor) * (static_cast<size_t>(count) + 1),
+                        cudaMemcpyHostToDevice, st) != cudaSuccess)
+      rc = QLORA_ERR_CUDA;
+  }
+  delete[] host;
+  delete head;
+  return rc;
+}
+
+int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t state_elems, const void* const* grads,
+                           int grad_dtype, const qlora_adamw_state_t* state, const qlora_adamw_t* hp, void* stream) {
+  if (!grads || !state || !hp || !state->m || !state->v || !state->steps) return QLORA_ERR_NULL;
+  if (count < 1 || count > kMaxTensors || state_elems < MA_BLOCK || state_elems % MA_BLOCK != 0)
+    return QLORA_ERR_SHAPE;
+  if (state->bits != 8 && state->bits != 32) return QLORA_ERR_UNSUPPORTED;
+  if (grad_dtype != QLORA_DTYPE_F32 && grad_dtype != QLORA_DTYPE_BF16) return QLORA_ERR_UNSUPPORTED;
+  if (state->bits == 8 && (!state->m_scale || !state->v_scale)) return QLORA_ERR_NULL;
+  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f && hp->eps > 0.0f &&
+        hp->lr >= 0.0f && hp->weight_decay >= 0.0f && std::isfinite(hp->max_grad_norm)))
+    return QLORA_ERR_UNSUPPORTED;
+  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(plan) || !aligned16(state->m) || !aligned16(state->v)) return QLORA_ERR_ALIGN;
+  const uintptr_t gmask = grad_dtype == QLORA_DTYPE_F32 ? 3u : 1u;
+  bool any = false;
+  for (int i = 0; i < count; ++i) {
+    if (reinterpret_cast<uintptr_t>(grads[i]) & gmask) return QLORA_ERR_ALIGN;
+    any = any || grads[i];
+  }
+  if (!any) return QLORA_OK;  // nothing has a gradient
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const MultiPlan mp = multi_plan_layout(plan, count);
+  MultiAdamWParams a{};
+  a.head = mp.head;
+  a.tensors = mp.tensors;
+  a.coef = mp.coef;
+  a.stored = mp.stored;
+  a.count = count;
+  a.from_memory = count > MA_PTRS ? 1 : 0;
+  a.m = state->m;
+  a.v = state->v;
+  a.m_scale = state->m_scale;
+  a.v_scale = state->v_scale;
+  a.steps = state->steps;
+  a.lr = hp->lr;
+  a.beta1 = hp->beta1;
+  a.beta2 = hp->beta2;
+  a.eps = hp->eps;
+  a.weight_decay = hp->weight_decay;
+  a.max_grad_norm = hp->max_grad_norm;
+  a.clip = hp->max_grad_norm > 0.0f ? 1 : 0;
+  GradPtrs gp{};
+  if (!a.from_memory) {
+    std::memcpy(gp.g, grads, sizeof(void*) * static_cast<size_t>(count));
+  } else {
+    for (int i = 0; i < count; i += MA_PTRS) {
+      const int n = count - i < MA_PTRS ? count - i : MA_PTRS;
+      std::memcpy(gp.g, grads + i, sizeof(void*) * static_cast<size_t>(n));
+      LaunchScope ls(QLORA_KERNEL_OPTIM, st);
+      multi_adamw_ptrs_kernel<<<4, 128, 0, st>>>(gp, mp.stored + i, n);
+    }
+    if (launch_status() != QLORA_OK) return QLORA_ERR_CUDA;
+  }
+  const int64_t blocks = state_elems / MA_BLOCK;
+  const bool f32 = grad_dtype == QLORA_DTYPE_F32;
+  if (state->bits == 8)
+    return f32 ? launch_multi_adamw<true, float>(a, gp, blocks, st) : launch_multi_adamw<true, uint16_t>(a, gp, blocks, st);
+  return f32 ? launch_multi_adamw<false, float>(a, gp, blocks, st) : launch_multi_adamw<false, uint16_t>(a, gp, blocks, st);
 }
 
 int qlora_merge_bf16(const qlora_nf4_t* Wq, const void* L1, const void* L2, int r, float s, void* out,

@@ -290,6 +290,64 @@ int qlora_grad_sqnorm(const float* g, int64_t n, double* acc, void* stream);
 int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16_t* param_bf16,
                      int64_t n, const qlora_adamw_t* hp, const double* sqnorm, void* stream);
 
+/* AdamW over many tensors (the L1, L2 factors of every linear and adapter) in
+ * two launches: the same step as qlora_adamw_step with clipping by the global
+ * norm of all gradients, per-tensor step counts kept on the device, and the
+ * moments in 32 or in 8 bits.  No counterpart on the pages beyond the recipe
+ * and the paged state above; the 8-bit form stores the moments the way §3
+ * stores the block constants.
+ *
+ * State: flat arrays over all tensors, tensor i starting at the element
+ * state offset sum_{j < i} ceil(n_j / 256) * 256, so that every block of
+ * QLORA_STATE_BLOCK = 256 elements belongs to one tensor; N is the total,
+ * qlora_multi_adamw_state_elems().  Elements behind a tensor's end are not used.
+ *   state_bits 32: m, v fp32 [N]; m_scale, v_scale NULL.
+ *   state_bits 8 : m, v uint8 [N], E4M3 codes of m and of r = sqrt(v);
+ *     m_scale, v_scale fp32 [N / 256].  A block x with largest magnitude a stores
+ *     scale = fp32(a / 448), code = E4M3_rn(fp32(x fp32(448 / a))) and stands for
+ *     fp32(E4M3(code) scale); zeros when a < 2^-100.  A positive r never takes
+ *     the code 0 but the next, 2^-9.  The update uses m and r before they are
+ *     rounded to codes.
+ *   steps: int32 [count], completed steps of each tensor; the call adds 1 where
+ *     there is a gradient, on the device, so a captured step replays as the next.
+ * Zero-initialised state (scales too) is the start of training.
+ *
+ * qlora_multi_adamw_plan: writes the table of `count` tensors (host array) into
+ *   `plan`, device memory of qlora_multi_adamw_plan_size(count) bytes, ordered on
+ *   `stream`; not during stream capture (QLORA_ERR_UNSUPPORTED).  The plan also
+ *   holds the partial sums of a step: steps that share one plan must be ordered.
+ *   param : fp32 [n], updated in place, 4-byte aligned (16 is faster);
+ *   copy  : bf16 [n] or NULL, receives bf16(param);  n >= 1.
+ * qlora_multi_adamw_step: one step.
+ *   grads : host array of `count` device pointers, fp32 or bf16 [n] as
+ *           grad_dtype says, element-aligned; NULL leaves the tensor, its state
+ *           and its step count as they are.  Not modified.
+ *   hp    : step is not used (see steps); max_grad_norm <= 0: no clipping.
+ *   A gradient with NaN or infinity: the norm clips nothing (NaN) or everything
+ *   (infinity), as in qlora_adamw_step; its element becomes NaN, and in 8 bits
+ *   its block of state does.                                              */
+#define QLORA_STATE_BLOCK 256
+typedef struct qlora_adamw_tensor_t {
+    float*    param;
+    uint16_t* copy;
+    int64_t   n;
+} qlora_adamw_tensor_t;
+typedef struct qlora_adamw_state_t {
+    void*    m;
+    void*    v;
+    float*   m_scale;
+    float*   v_scale;
+    int32_t* steps;
+    int32_t  bits;
+} qlora_adamw_state_t;
+int64_t qlora_multi_adamw_state_elems(const qlora_adamw_tensor_t* tensors, int count);
+size_t qlora_multi_adamw_plan_size(int count);
+int qlora_multi_adamw_plan(const qlora_adamw_tensor_t* tensors, int count, void* plan, size_t plan_bytes,
+                           void* stream);
+int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t state_elems,
+                           const void* const* grads, int grad_dtype, const qlora_adamw_state_t* state,
+                           const qlora_adamw_t* hp, void* stream);
+
 /* qlora_merge_bf16 - merge the trained adapter into the 16-bit dequantized
  * base (QLoRA glossary, pitfalls entry: merge into the bf16 dequantized base,
  * never into the 4-bit codes; walkthrough "推理": the adapter can also stay
