@@ -110,8 +110,13 @@ __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const
 constexpr int MA_BLOCK = 256;
 constexpr int MA_THREADS = 256;
 constexpr int MA_WARPS = MA_THREADS / 32;
+// Resident CTAs of the update.  Registers for the prefetched block against
+// warps: 8 bits 722 / 705 / 751 us a step of 160 M parameters at 2 / 3 / 4 CTAs,
+// 32 bits 895 / 984 at 2 / 3.
+constexpr int MA_PER_SM8 = 3, MA_PER_SM32 = 2;
 constexpr int MA_PTRS = 496;          // gradient pointers passed with a launch (under 4 KB of parameters)
 constexpr int MA_NORM_CTAS = 148 * 4; // partial sums of the norm, one per CTA
+constexpr int MA_UNROLL = 4;          // blocks of gradients a warp loads at a time for the norm
 
 struct MultiTensor {
   float* p;         // fp32 [n]
@@ -123,6 +128,7 @@ struct MultiTensor {
 struct MultiCoef {
   float step_size;  // lr / (1 - beta1^t), t the tensor's own step count
   float bc2_sqrt;   // sqrt(1 - beta2^t)
+  float bc2_inv;    // 1 / sqrt(1 - beta2^t)
 };
 
 // Device side of a plan, in this order in one allocation.
@@ -236,27 +242,30 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
   if (a.clip) {
     const int64_t blocks = a.head->blocks;
     const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
-    int t = -1;
-    int64_t next = 0, first = 0, n = 0;
-    const G* g = nullptr;
-    bool vec = false;
-    for (int64_t b = b0 + warp; b < b1; b += MA_WARPS) {
-      if (t < 0 || b >= next) {
-        t = t < 0 ? multi_find(a.tensors, a.count, b) : t + 1;
-        while (a.tensors[t + 1].block0 <= b) ++t;
-        first = a.tensors[t].block0;
-        next = a.tensors[t + 1].block0;
-        n = a.tensors[t].n;
-        g = static_cast<const G*>(multi_grad(a, gp, t));
-        vec = vec_ok(g, 4 * sizeof(G));
-      }
-      if (!g) continue;
-      const int64_t e = (b - first) * MA_BLOCK;
-      const int left = static_cast<int>(n - e < MA_BLOCK ? n - e : MA_BLOCK);
-      float x[8];
-      load8<G>(g + e, left, vec, lane, x);
+    int t = b0 < b1 ? multi_find(a.tensors, a.count, b0) : 0;
+    for (int64_t b = b0; b < b1; ++t) {
+      const MultiTensor ts = a.tensors[t];
+      const int64_t next = a.tensors[t + 1].block0;
+      const int64_t end = next < b1 ? next : b1;
+      const G* g = static_cast<const G*>(multi_grad(a, gp, t));
+      if (g) {
+        const bool vec = vec_ok(g, 4 * sizeof(G));
+        // four blocks a warp at a time: 4 KB of loads in flight
+        for (int64_t k = b + warp; k < end; k += MA_UNROLL * MA_WARPS) {
+          float x[MA_UNROLL][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += static_cast<double>(x[j]) * x[j];
+          for (int u = 0; u < MA_UNROLL; ++u) {
+            const int64_t e = (k + u * MA_WARPS - ts.block0) * MA_BLOCK;
+            const int64_t left = k + u * MA_WARPS < end ? ts.n - e : 0;
+            load8<G>(g + e, static_cast<int>(left < MA_BLOCK ? left : MA_BLOCK), vec, lane, x[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < MA_UNROLL; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += static_cast<double>(x[u][j]) * x[u][j];
+        }
+      }
+      b = end;
     }
   }
 #pragma unroll
@@ -278,7 +287,9 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
     const int k = ++a.steps[t];
     MultiCoef c;
     c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k)));
-    c.bc2_sqrt = static_cast<float>(sqrt(1.0 - pow(static_cast<double>(a.beta2), k)));
+    const double root = sqrt(1.0 - pow(static_cast<double>(a.beta2), k));
+    c.bc2_sqrt = static_cast<float>(root);
+    c.bc2_inv = static_cast<float>(1.0 / root);
     a.coef[t] = c;
   }
   if (warp == 0) {
@@ -326,10 +337,23 @@ __device__ __forceinline__ void state_decode(uint2 w, float scale, float (&x)[8]
     }
 }
 
+// Square root (subnormal arguments included: the roots of small v count) and
+// reciprocal to 1 ulp.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // The scale of a block and the factor of its codes, from the largest
-// magnitude's bits.  Blocks below 2^-100 (448 / max would overflow) hold zeros;
-// a NaN or an infinity makes the scale one of the two, so that its block
-// decodes to NaN.
+// magnitude's bits.  Blocks below 2^-100 (448 / max would overflow) hold zeros.
+// A NaN does not count (it has a code of its own); an infinity makes the scale
+// infinite, and its block decodes to NaN.
 __device__ __forceinline__ void block_scale(uint32_t top_bits, float& scale, float& inv) {
   const float top = __uint_as_float(top_bits);
   const bool dead = top < 0x1p-100f;
@@ -337,106 +361,141 @@ __device__ __forceinline__ void block_scale(uint32_t top_bits, float& scale, flo
   inv = dead ? 0.0f : __fdiv_rn(448.0f, top);
 }
 
-// The update, in adamw_kernel's order and rounding (fp32 IEEE throughout).  A
-// warp takes whole blocks of its CTA's contiguous range, from the end to the
-// beginning: the norm read the range upwards, so the gradients it read last
-// are still in L2.
+// What a lane reads of a block.
+template <bool k8>
+struct MultiLoads {
+  float g[8], p[8];
+  float m[k8 ? 1 : 8], v[k8 ? 1 : 8];  // 32-bit state
+  uint2 mw, vw;                        // 8-bit state: codes and scales
+  float ms, vs;
+};
+
+// The update.  Every CTA has a contiguous range of blocks, which its warps take
+// in turn from the end to the beginning: the norm read the range upwards, so
+// the gradients it read last are still in L2.  A warp loads its next block of
+// the tensor before it computes the present one.
+//   32 bits: adamw_kernel's order and rounding (fp32 IEEE throughout), so the
+//   result is that of qlora_adamw_step bit for bit; bound by DRAM.
+//   8 bits: with IEEE square roots and divisions the kernel is bound by
+//   instruction issue, not by DRAM (a step over 160 M parameters: 990 us, with
+//   the approximate root, reciprocal and fused multiply-adds below 705 us); they
+//   cost 4 ulp of the update, far below p's own rounding.
 template <bool k8, typename G>
-__global__ void __launch_bounds__(MA_THREADS) multi_adamw_kernel(const __grid_constant__ MultiAdamWParams a,
-                                                                 const __grid_constant__ GradPtrs gp) {
+__global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
+    multi_adamw_kernel(const __grid_constant__ MultiAdamWParams a, const __grid_constant__ GradPtrs gp) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blocks = a.head->blocks;
   const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
   const float decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
   const float one_m_b1 = __fsub_rn(1.0f, a.beta1), one_m_b2 = __fsub_rn(1.0f, a.beta2);
+  if (b0 >= b1) return;
   pdl_wait();  // coefficients, and the step before this one
   const float clip = __ldcg(&a.head->clip);
-  int t = -1;
-  int64_t first = 0;
-  MultiTensor ts{};
-  MultiCoef c{};
-  const G* g = nullptr;
-  bool vec = false, gvec = false;
-  for (int64_t b = b1 - 1 - warp; b >= b0; b -= MA_WARPS) {
-    if (t < 0 || b < first) {
-      t = t < 0 ? multi_find(a.tensors, a.count, b) : t - 1;
-      while (a.tensors[t].block0 > b) --t;
-      ts = a.tensors[t];
-      first = ts.block0;
-      g = static_cast<const G*>(multi_grad(a, gp, t));
-      if (g) {
-        c.step_size = __ldcg(&a.coef[t].step_size);
-        c.bc2_sqrt = __ldcg(&a.coef[t].bc2_sqrt);
+  int t = multi_find(a.tensors, a.count, b1 - 1);
+  for (int64_t top = b1; top > b0; --t) {
+    const MultiTensor ts = a.tensors[t];
+    const int64_t lo = ts.block0 > b0 ? ts.block0 : b0;
+    const G* g = static_cast<const G*>(multi_grad(a, gp, t));
+    if (!g) {
+      top = lo;
+      continue;
+    }
+    const float step_size = __ldcg(&a.coef[t].step_size);
+    const float root = __ldcg(k8 ? &a.coef[t].bc2_inv : &a.coef[t].bc2_sqrt);
+    const bool vec = vec_ok(ts.p, 16) && vec_ok(ts.copy, 8), gvec = vec_ok(g, 4 * sizeof(G));
+    auto left_of = [&](int64_t b) -> int {
+      const int64_t n = ts.n - (b - ts.block0) * MA_BLOCK;
+      return static_cast<int>(n < MA_BLOCK ? n : MA_BLOCK);
+    };
+    auto load = [&](int64_t b, MultiLoads<k8>& x) {
+      const int64_t e = (b - ts.block0) * MA_BLOCK;
+      const int left = left_of(b);
+      load8<G>(g + e, left, gvec, lane, x.g);
+      load8<float>(ts.p + e, left, vec, lane, x.p);
+      if constexpr (k8) {  // the flat state is padded to whole blocks
+        const uint32_t* mc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + b * MA_BLOCK) + lane;
+        const uint32_t* vc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + b * MA_BLOCK) + lane;
+        x.mw = make_uint2(mc[0], mc[32]);
+        x.vw = make_uint2(vc[0], vc[32]);
+        x.ms = a.m_scale[b];
+        x.vs = a.v_scale[b];
+      } else {
+        load8<float>(static_cast<const float*>(a.m) + b * MA_BLOCK, MA_BLOCK, true, lane, x.m);
+        load8<float>(static_cast<const float*>(a.v) + b * MA_BLOCK, MA_BLOCK, true, lane, x.v);
       }
-      vec = vec_ok(ts.p, 16) && vec_ok(ts.copy, 8);
-      gvec = vec_ok(g, 4 * sizeof(G));
-    }
-    if (!g) continue;
-    const int64_t e = (b - first) * MA_BLOCK;
-    const int left = static_cast<int>(ts.n - e < MA_BLOCK ? ts.n - e : MA_BLOCK);
-    float p[8], x[8], m[8], v[8];
-    load8<G>(g + e, left, gvec, lane, x);
-    load8<float>(ts.p + e, left, vec, lane, p);
-    const int64_t at = b * MA_BLOCK + 4 * lane;  // the flat state is padded to whole blocks
-    if constexpr (k8) {
-      const uint8_t* mc = static_cast<const uint8_t*>(a.m) + at;
-      const uint8_t* vc = static_cast<const uint8_t*>(a.v) + at;
-      const uint2 mw = make_uint2(*reinterpret_cast<const uint32_t*>(mc), *reinterpret_cast<const uint32_t*>(mc + 128));
-      const uint2 vw = make_uint2(*reinterpret_cast<const uint32_t*>(vc), *reinterpret_cast<const uint32_t*>(vc + 128));
-      state_decode(mw, a.m_scale[b], m);
-      state_decode(vw, a.v_scale[b], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
-    } else {
-      load8<float>(static_cast<const float*>(a.m) + b * MA_BLOCK, MA_BLOCK, true, lane, m);
-      load8<float>(static_cast<const float*>(a.v) + b * MA_BLOCK, MA_BLOCK, true, lane, v);
-    }
-    float r[8];
-    uint32_t mtop = 0, rtop = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float gi = __fmul_rn(x[j], clip);
-      m[j] = __fadd_rn(m[j], __fmul_rn(one_m_b1, __fsub_rn(gi, m[j])));
-      v[j] = __fadd_rn(__fmul_rn(a.beta2, v[j]), __fmul_rn(one_m_b2, __fmul_rn(gi, gi)));
-      r[j] = __fsqrt_rn(v[j]);
-      const float denom = __fadd_rn(__fdiv_rn(r[j], c.bc2_sqrt), a.eps);
-      p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(c.step_size, __fdiv_rn(m[j], denom)));
+    };
+    int64_t b = top - 1 - warp;
+    MultiLoads<k8> cur, nxt;
+    if (b >= lo) load(b, cur);
+    for (; b >= lo; b -= MA_WARPS) {
+      if (b - MA_WARPS >= lo) load(b - MA_WARPS, nxt);
+      const int64_t e = (b - ts.block0) * MA_BLOCK;
+      const int left = left_of(b);
+      float(&p)[8] = cur.p;
+      float m[8], r[8], v[8];
       if constexpr (k8) {
-        // what lies behind the tensor's end does not count for the block
-        if (128 * (j >> 2) + 4 * lane + (j & 3) >= left) m[j] = r[j] = 0.0f;
-        mtop = max(mtop, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-        rtop = max(rtop, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-      }
-    }
-    store8(ts.p + e, left, vec, lane, p);
-    if (ts.copy) {
+        state_decode(cur.mw, cur.ms, m);
+        state_decode(cur.vw, cur.vs, r);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = 128 * h + 4 * lane;
-        const uint32_t w0 = pack_bf16x2(p[4 * h], p[4 * h + 1]), w1 = pack_bf16x2(p[4 * h + 2], p[4 * h + 3]);
-        if (vec && i + 4 <= left) {
-          *reinterpret_cast<uint2*>(ts.copy + e + i) = make_uint2(w0, w1);
-        } else {
+        for (int j = 0; j < 8; ++j) {
+          const float gi = cur.g[j] * clip;
+          m[j] = fmaf(one_m_b1, gi - m[j], m[j]);
+          r[j] = sqrt_approx(fmaf(a.beta2 * r[j], r[j], one_m_b2 * gi * gi));
+          p[j] = fmaf(p[j], decay, -step_size * (m[j] * rcp_approx(fmaf(r[j], root, a.eps))));
+        }
+        if (left < MA_BLOCK) {  // what lies behind the tensor's end does not count for the block
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (i + j < left) ts.copy[e + i + j] = static_cast<uint16_t>((j < 2 ? w0 : w1) >> (16 * (j & 1)));
+          for (int j = 0; j < 8; ++j)
+            if (128 * (j >> 2) + 4 * lane + (j & 3) >= left) m[j] = r[j] = 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float gi = __fmul_rn(cur.g[j], clip);
+          m[j] = __fadd_rn(cur.m[j], __fmul_rn(one_m_b1, __fsub_rn(gi, cur.m[j])));
+          v[j] = __fadd_rn(__fmul_rn(a.beta2, cur.v[j]), __fmul_rn(one_m_b2, __fmul_rn(gi, gi)));
+          const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v[j]), root), a.eps);
+          p[j] = __fsub_rn(__fmul_rn(p[j], decay), __fmul_rn(step_size, __fdiv_rn(m[j], denom)));
         }
       }
+      store8(ts.p + e, left, vec, lane, p);
+      if (ts.copy) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = 128 * h + 4 * lane;
+          const uint32_t w0 = pack_bf16x2(p[4 * h], p[4 * h + 1]), w1 = pack_bf16x2(p[4 * h + 2], p[4 * h + 3]);
+          if (vec && i + 4 <= left) {
+            *reinterpret_cast<uint2*>(ts.copy + e + i) = make_uint2(w0, w1);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (i + j < left) ts.copy[e + i + j] = static_cast<uint16_t>((j < 2 ? w0 : w1) >> (16 * (j & 1)));
+          }
+        }
+      }
+      if constexpr (k8) {
+        float mtop = 0.0f, rtop = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          mtop = fmaxf(mtop, fabsf(m[j]));
+          rtop = fmaxf(rtop, r[j]);
+        }
+        float ms, minv, rs, rinv;
+        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mtop)), ms, minv);
+        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rtop)), rs, rinv);
+        const uint2 mw = state_encode<false>(m, minv), vw = state_encode<true>(r, rinv);
+        uint32_t* mc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + b * MA_BLOCK) + lane;
+        uint32_t* vc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + b * MA_BLOCK) + lane;
+        mc[0] = mw.x, mc[32] = mw.y;
+        vc[0] = vw.x, vc[32] = vw.y;
+        if (lane == 0) a.m_scale[b] = ms, a.v_scale[b] = rs;
+      } else {
+        store8(static_cast<float*>(a.m) + b * MA_BLOCK, left, true, lane, m);
+        store8(static_cast<float*>(a.v) + b * MA_BLOCK, left, true, lane, v);
+      }
+      cur = nxt;
     }
-    if constexpr (k8) {
-      float ms, minv, rs, rinv;
-      block_scale(__reduce_max_sync(0xFFFFFFFFu, mtop), ms, minv);
-      block_scale(__reduce_max_sync(0xFFFFFFFFu, rtop), rs, rinv);
-      const uint2 mw = state_encode<false>(m, minv), vw = state_encode<true>(r, rinv);
-      uint8_t* mc = static_cast<uint8_t*>(a.m) + at;
-      uint8_t* vc = static_cast<uint8_t*>(a.v) + at;
-      *reinterpret_cast<uint32_t*>(mc) = mw.x, *reinterpret_cast<uint32_t*>(mc + 128) = mw.y;
-      *reinterpret_cast<uint32_t*>(vc) = vw.x, *reinterpret_cast<uint32_t*>(vc + 128) = vw.y;
-      if (lane == 0) a.m_scale[b] = ms, a.v_scale[b] = rs;
-    } else {
-      store8(static_cast<float*>(a.m) + b * MA_BLOCK, left, true, lane, m);
-      store8(static_cast<float*>(a.v) + b * MA_BLOCK, left, true, lane, v);
-    }
+    top = lo;
   }
 }
 

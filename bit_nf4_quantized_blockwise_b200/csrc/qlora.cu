@@ -1225,7 +1225,7 @@ int launch_multi_adamw(const MultiAdamWParams& a, const GradPtrs& gp, int64_t bl
     multi_adamw_prepare_kernel<G><<<static_cast<unsigned>(norm), MA_THREADS, 0, st>>>(a, gp);
   }
   if (launch_status() != QLORA_OK) return QLORA_ERR_CUDA;
-  const int64_t most = static_cast<int64_t>(sm_count()) * 4;
+  const int64_t most = static_cast<int64_t>(sm_count()) * (k8 ? MA_PER_SM8 : MA_PER_SM32);
   LaunchScope ls(QLORA_KERNEL_OPTIM, st);
   // programmatic dependent launch: the update's blocks are set up while the norm is summed
   cudaLaunchConfig_t cfg{};

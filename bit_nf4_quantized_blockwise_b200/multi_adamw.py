@@ -8,7 +8,9 @@ parameter buffer.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 from typing import Callable, Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
@@ -18,6 +20,9 @@ from ._lib import (QLORA_DTYPE_BF16, QLORA_DTYPE_F32, _check, _stream, lib, qlor
 from .paged import AdamWConfig, ManagedBuffer, PagingPolicy
 
 STATE_BLOCK = 256
+
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+_device, _contiguous, _data_ptr = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
 
 
 class MultiAdamW:
@@ -104,7 +109,6 @@ class MultiAdamW:
             st.m_scale, st.v_scale = self.m_scale.data_ptr(), self.v_scale.data_ptr()
         st.steps, st.bits = self.steps.data_ptr(), self.state_bits
         self._struct = st
-        self._ptrs = (ctypes.c_void_p * n)()
 
     def _move(self, to_host: bool) -> None:
         for b in self._buffers:
@@ -125,33 +129,39 @@ class MultiAdamW:
         params[i]) or None, which leaves parameter, state and step count i as
         they are.  The gradients are not modified.  May be captured into a CUDA
         graph: the step counts live on the device."""
+        grads = list(grads)
         if len(grads) != len(self._numel):
             raise ValueError(f"{len(grads)} grads for {len(self._numel)} params")
-        dtype = None
-        dev, ptrs = self.device, self._ptrs
-        for i, g in enumerate(grads):
-            if g is None:
-                ptrs[i] = None
-                continue
-            if g.dtype is not dtype:
-                if dtype is not None:
-                    raise ValueError(f"grads[{i}] is {g.dtype}, the ones before it {dtype}")
-                dtype = g.dtype
-            if g.shape != self._shapes[i] or g.device != dev or not g.is_contiguous():
-                raise ValueError(f"grads[{i}] must be a contiguous tensor of shape {tuple(self._shapes[i])} on {dev}")
-            ptrs[i] = g.data_ptr()
-        if dtype is None:
+        at = [i for i, g in enumerate(grads) if g is not None]
+        if not at:
             return
-        if dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError(f"grads must be fp32 or bf16, not {dtype}")
+        given, shapes = grads, self._shapes
+        if len(at) < len(grads):
+            given, shapes = [grads[i] for i in at], [self._shapes[i] for i in at]
+        # whole lists at once: a model has hundreds of tensors, and a step takes a few hundred microseconds
+        dtypes = set(map(_dtype, given))
+        if len(dtypes) != 1 or not dtypes <= {torch.float32, torch.bfloat16}:
+            raise ValueError(f"grads must all be fp32 or all be bf16, not {sorted(map(str, dtypes))}")
+        if list(map(_shape, given)) != shapes or set(map(_device, given)) != {self.device.index} or \
+                not all(map(_contiguous, given)):
+            for i, g, s in zip(at, given, shapes):
+                if g.shape != s or g.device != self.device or not g.is_contiguous():
+                    raise ValueError(f"grads[{i}] must be a contiguous tensor of shape {tuple(s)} on {self.device}")
+        found = list(map(_data_ptr, given))
+        if len(at) < len(grads):
+            ptrs = [0] * len(grads)
+            for i, x in zip(at, found):
+                ptrs[i] = x
+            found = ptrs
+        ptrs = (ctypes.c_uint64 * len(found)).from_buffer(array.array("Q", found))
         if self._buffers and (self.watermark > 0 or self.policy.on_host):
             self.policy.on_step()
-        c = self.cfg
+        c, dev = self.cfg, self.device
         hp = qlora_adamw_t(c.lr, c.beta1, c.beta2, c.eps, c.weight_decay, float(c.max_grad_norm or 0.0), 0)
         with torch.cuda.device(dev):
             _check(lib().qlora_multi_adamw_step(
                 ctypes.c_void_p(self._plan.data_ptr()), self._plan.numel(), len(self._numel), self._elems, ptrs,
-                QLORA_DTYPE_F32 if dtype == torch.float32 else QLORA_DTYPE_BF16, ctypes.byref(self._struct),
+                QLORA_DTYPE_F32 if torch.float32 in dtypes else QLORA_DTYPE_BF16, ctypes.byref(self._struct),
                 ctypes.byref(hp), _stream(dev)), "qlora_multi_adamw_step")
 
     def moments(self, i: int) -> Tuple[torch.Tensor, torch.Tensor]:

@@ -324,8 +324,10 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
  *           and its step count as they are.  Not modified.
  *   hp    : step is not used (see steps); max_grad_norm <= 0: no clipping.
  *   A gradient with NaN or infinity: the norm clips nothing (NaN) or everything
- *   (infinity), as in qlora_adamw_step; its element becomes NaN, and in 8 bits
- *   its block of state does.                                              */
+ *   (infinity), as in qlora_adamw_step; its element becomes NaN, and with
+ *   8-bit state an infinity makes its whole block of state NaN.
+ * With 32-bit state the results are those of qlora_adamw_step bit for bit; with
+ * 8-bit state the root and the quotient of the update are good to 4 ulp.     */
 #define QLORA_STATE_BLOCK 256
 typedef struct qlora_adamw_tensor_t {
     float*    param;
