@@ -6,11 +6,14 @@ dequant-GEMM forward / backward of Y = X W' + s X L1 L2.  All arithmetic runs
 in hand-written sm_100a CUDA kernels; this package only marshals arguments.
 """
 from ._lib import (  # noqa: F401
+    AdapterBank,
+    AdapterPlan,
     EXPORTS,
     LIB_PATH,
     NF4Weight,
     QLoRAError,
     lib,
+    qlora_adapter_plan,
     qlora_check_status,
     qlora_launch_count,
     qlora_trace_enable,
@@ -21,6 +24,8 @@ from ._lib import (  # noqa: F401
     qlora_linear_fwd,
     qlora_linear_fwd_noalloc,
     qlora_merge_bf16,
+    qlora_multi_linear_bwd,
+    qlora_multi_linear_fwd,
     qlora_nf4_boundaries,
     qlora_nf4_codebook,
     qlora_quantize_nf4,

@@ -45,6 +45,11 @@ class qlora_adamw_state_t(ctypes.Structure):
                 ("steps", _c_void_p), ("bits", ctypes.c_int32)]
 
 
+class qlora_adapters_t(ctypes.Structure):
+    """Mirror of the C struct qlora_adapters_t."""
+    _fields_ = [("L1", _c_void_p), ("L2", _c_void_p), ("s", _c_void_p), ("n", ctypes.c_int32), ("r", ctypes.c_int32)]
+
+
 class qlora_nf4_t(ctypes.Structure):
     """Mirror of the C struct qlora_nf4_t."""
     _fields_ = [
@@ -95,6 +100,16 @@ EXPORTS = {
     "qlora_grad_sqnorm": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p]),
     "qlora_adamw_step": (_c_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_i64, _c_void_p,
                                   _c_void_p, _c_void_p]),
+    "qlora_adapter_plan_size": (_c_size, [_c_i64, _c_int]),
+    "qlora_adapter_plan": (_c_int, [_c_void_p, _c_i64, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "qlora_multi_linear_fwd_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "qlora_multi_linear_bwd_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "qlora_multi_linear_fwd": (_c_int, [ctypes.POINTER(qlora_nf4_t), _c_void_p, _c_i64,
+                                        ctypes.POINTER(qlora_adapters_t), _c_void_p, _c_size, _c_void_p, _c_int,
+                                        _c_void_p, _c_void_p, _c_size, _c_void_p]),
+    "qlora_multi_linear_bwd": (_c_int, [ctypes.POINTER(qlora_nf4_t), _c_void_p, _c_void_p, _c_i64,
+                                        ctypes.POINTER(qlora_adapters_t), _c_void_p, _c_size, _c_void_p, _c_void_p,
+                                        _c_int, _c_void_p, _c_void_p, _c_void_p, _c_size, _c_void_p]),
     "qlora_multi_adamw_state_elems": (_c_i64, [_c_void_p, _c_int]),
     "qlora_multi_adamw_plan_size": (_c_size, [_c_int]),
     "qlora_multi_adamw_plan": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_size, _c_void_p]),
@@ -447,6 +462,147 @@ def qlora_merge_bf16(Wq: NF4Weight, L1: torch.Tensor, L2: torch.Tensor, s: float
         _check(lib().qlora_merge_bf16(ctypes.byref(st), _p(L1), _p(L2), r, float(s), _p(out), _stream(dev)),
                "qlora_merge_bf16")
     return out
+
+
+@dataclass
+class AdapterBank:
+    """Adapters that share one frozen weight: bf16 L1 [n][h][r] and L2 [n][r][o]
+    (adapters of smaller rank padded with zeros), fp32 scales s [n] on the
+    device.  Views of one adapter (bank.L1[a]) are its factors."""
+    L1: torch.Tensor
+    L2: torch.Tensor
+    s: torch.Tensor
+
+    def __post_init__(self):
+        if self.L1.dim() != 3 or self.L2.dim() != 3:
+            raise ValueError("L1 must be (n, h, r) and L2 (n, r, o)")
+        n, h, r = self.L1.shape
+        _need(self.L1, "L1", (n, h, r), (torch.bfloat16,))
+        _need(self.L2, "L2", (n, r, self.L2.shape[2]), (torch.bfloat16,))
+        _need(self.s, "s", (n,), (torch.float32,))
+        _same_device(self.L1, self.L2, self.s)
+
+    @property
+    def n(self) -> int:
+        return self.L1.shape[0]
+
+    @property
+    def r(self) -> int:
+        return self.L1.shape[2]
+
+    def struct(self) -> qlora_adapters_t:
+        return qlora_adapters_t(self.L1.data_ptr(), self.L2.data_ptr(), self.s.data_ptr(), self.n, self.r)
+
+
+@dataclass
+class AdapterPlan:
+    """The tokens of a batch grouped by adapter (qlora_adapter_plan)."""
+    buffer: torch.Tensor
+    M: int
+    n: int
+
+
+def qlora_adapter_plan(adapter: torch.Tensor, n: int, plan: Optional[AdapterPlan] = None) -> AdapterPlan:
+    """Groups a batch's tokens by adapter: int32 adapter [M] with the index of
+    each token's adapter in a bank of n, or -1 for none.  Once per batch: the
+    plan serves every layer and both passes.  ``plan``: one of the same M and n
+    to be overwritten (as a captured graph needs)."""
+    if adapter.dim() != 1 or adapter.dtype != torch.int32:
+        raise ValueError(f"adapter must be a 1-D int32 tensor, not {adapter.dtype} {tuple(adapter.shape)}")
+    M = adapter.shape[0]
+    if M < 1:
+        raise ValueError("adapter is empty")
+    L = lib()
+    size = L.qlora_adapter_plan_size(M, n)
+    if size == 0:
+        raise ValueError(f"a plan of {M} tokens and {n} adapters is not supported")
+    if plan is not None and (plan.M != M or plan.n != n):
+        raise ValueError(f"plan is for {plan.M} tokens and {plan.n} adapters, not {M} and {n}")
+    _same_device(adapter, None if plan is None else plan.buffer)
+    dev = _require_cuda(adapter)
+    if plan is None:
+        plan = AdapterPlan(torch.empty(size, dtype=torch.uint8, device=dev), M, int(n))
+    with torch.cuda.device(dev):
+        _check(L.qlora_adapter_plan(_p(adapter), M, plan.n, _p(plan.buffer), plan.buffer.numel(), _stream(dev)),
+               "qlora_adapter_plan")
+    return plan
+
+
+def _check_multi(Wq: NF4Weight, X, bank: AdapterBank, plan: AdapterPlan, Y=None, T=None, dY=None, dX=None, dL1=None,
+                 dL2=None):
+    """Every operand of the many-adapter layer against the weight, the bank and the plan."""
+    _check_weight(Wq)
+    o, h = Wq.o, Wq.h
+    if X.dim() != 2 or X.shape[1] != h:
+        raise ValueError(f"X has shape {tuple(X.shape)}, expected (M, {h})")
+    M = X.shape[0]
+    n, hb, r = bank.L1.shape
+    if hb != h or bank.L2.shape[2] != o:
+        raise ValueError(f"the bank is for {hb} x {bank.L2.shape[2]}, the weight is {h} x {o}")
+    if plan.M != M or plan.n != n:
+        raise ValueError(f"plan is for {plan.M} tokens and {plan.n} adapters, not {M} and {n}")
+    _need(X, "X", (M, h), (torch.bfloat16,))
+    _need(Y, "Y", (M, o), (torch.float32, torch.bfloat16))
+    _need(T, "T", (M, r), (torch.float32,))
+    _need(dY, "dY", (M, o), (torch.bfloat16,))
+    _need(dX, "dX", (M, h), (torch.float32, torch.bfloat16))
+    _need(dL1, "dL1", (n, h, r), (torch.float32,))
+    _need(dL2, "dL2", (n, r, o), (torch.float32,))
+    _same_device(Wq.codes, Wq.absmax_fp8, Wq.dq_scale, Wq.dq_mean, Wq.absmax, X, bank.L1, plan.buffer, Y, T, dY, dX,
+                 dL1, dL2)
+    return M, n, r
+
+
+def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, plan: AdapterPlan,
+                           y_dtype: torch.dtype = torch.float32, save_T: bool = True,
+                           Y: Optional[torch.Tensor] = None, T_save: Optional[torch.Tensor] = None,
+                           ws: Optional[torch.Tensor] = None):
+    """Y_i = X_i W' + s[a_i] X_i L1[a_i] L2[a_i], each token with its own adapter
+    of the bank (or none).  Returns (Y, T), T_i = X_i L1[a_i] in fp32 (None
+    unless save_T)."""
+    M, n, r = _check_multi(Wq, X, bank, plan, Y=Y, T=T_save)
+    dev = _require_cuda(X, Wq.codes, bank.L1)
+    if Y is None:
+        Y = torch.empty(M, Wq.o, dtype=y_dtype, device=dev)
+    if T_save is None and save_T:
+        T_save = torch.empty(M, r, dtype=torch.float32, device=dev)
+    L = lib()
+    wsb = L.qlora_multi_linear_fwd_workspace_size(Wq.o, Wq.h, M, n, r)
+    if ws is None or ws.numel() * ws.element_size() < wsb:
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(L.qlora_multi_linear_fwd(ctypes.byref(Wq.struct()), _p(X), M, ctypes.byref(bank.struct()),
+                                        _p(plan.buffer), plan.buffer.numel(), _p(Y), _dtype_code(Y.dtype), _p(T_save),
+                                        _p(ws), ws.numel() * ws.element_size(), _stream(dev)),
+               "qlora_multi_linear_fwd")
+    return Y, T_save
+
+
+def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, bank: AdapterBank, plan: AdapterPlan,
+                           T_saved: Optional[torch.Tensor] = None, dx_dtype: torch.dtype = torch.float32,
+                           dX: Optional[torch.Tensor] = None, dL1: Optional[torch.Tensor] = None,
+                           dL2: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Returns (dX, dL1 [n][h][r], dL2 [n][r][o]) of <Y, dY>; adapters without
+    tokens get zero gradients, W is frozen."""
+    M, n, r = _check_multi(Wq, X, bank, plan, T=T_saved, dY=dY, dX=dX, dL1=dL1, dL2=dL2)
+    dev = _require_cuda(X, Wq.codes, bank.L1)
+    if dX is None:
+        dX = torch.empty(M, Wq.h, dtype=dx_dtype, device=dev)
+    if dL1 is None:
+        dL1 = torch.empty(n, Wq.h, r, dtype=torch.float32, device=dev)
+    if dL2 is None:
+        dL2 = torch.empty(n, r, Wq.o, dtype=torch.float32, device=dev)
+    L = lib()
+    wsb = L.qlora_multi_linear_bwd_workspace_size(Wq.o, Wq.h, M, n, r)
+    if ws is None or ws.numel() * ws.element_size() < wsb:
+        ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(L.qlora_multi_linear_bwd(ctypes.byref(Wq.struct()), _p(X), _p(dY), M, ctypes.byref(bank.struct()),
+                                        _p(plan.buffer), plan.buffer.numel(), _p(T_saved), _p(dX),
+                                        _dtype_code(dX.dtype), _p(dL1), _p(dL2), _p(ws),
+                                        ws.numel() * ws.element_size(), _stream(dev)),
+               "qlora_multi_linear_bwd")
+    return dX, dL1, dL2
 
 
 def qlora_check_status(device: Optional[torch.device] = None) -> None:

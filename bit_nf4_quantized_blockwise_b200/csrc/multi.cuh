@@ -1,0 +1,1005 @@
+// multi.cuh - the linear layer with many adapters beside one frozen weight:
+// token i uses adapter a_i of a bank (or none),
+//   Y_i  = X_i W' + s[a_i] T_i L2[a_i],         T_i = X_i L1[a_i]
+//   dX_i = dY_i W'^T + s[a_i] U_i L1[a_i]^T,    U_i = dY_i L2[a_i]^T
+//   dL1[a] = s[a] sum_{a_i = a} X_i^T U_i,  dL2[a] = s[a] sum_{a_i = a} T_i^T dY_i
+// (the LoRA equation of the walkthrough's background section and its training
+// step 5, with the factors chosen per token).
+//
+// adapter_plan_kernel sorts the tokens of a batch into groups of one adapter,
+// in the order of first appearance, so that a batch whose adapters are already
+// contiguous (whole requests one after the other) keeps its order and nothing
+// has to be moved.  Everything below works on sorted rows.
+//
+// The rank-r product of a group is appended to the K loop of the W' product, as
+// in the one-adapter GEMM, but per 256-row tile and only for the groups that
+// have rows in it: a *slot* is one (tile, group) pair and holds the group's
+// 256 x rp rows of s T as bf16 parts (hi, the rounding of what is left, and
+// again), with zeros in the rows of other groups.  A batch has at most
+// tiles + groups slots.
+//
+// Zero rows keep the groups apart only while the factors are finite: 0 times an
+// infinity or a NaN of another group's adapter (or of another token, in the
+// sums over tokens) is NaN.  Every element of a tile that several groups share
+// that comes out non-finite is therefore computed once more from its own row
+// and adapter alone, in fp32; a finite batch never gets there.
+#pragma once
+
+#include "common.cuh"
+#include "gemm.cuh"
+#include "pairgemm.cuh"
+
+namespace qlora {
+
+// ====================================================================== the plan of a batch
+
+constexpr int MP_THREADS = 1024;
+constexpr int MP_WARPS = MP_THREADS / 32;
+constexpr int MP_SLOT_ROWS = 256;  // rows of a slot: those of a pair tile
+constexpr int MP_TILE = 64;        // rows of a tile of the rank-r products
+
+struct PlanHead {
+  int groups;    // adapters with tokens
+  int in_order;  // the sorted order is the batch's own
+  int slots;
+  int tiles;     // 64-row tiles of the groups
+};
+
+// Arrays of a plan (device); lengths in brackets, G = min(n, M).
+struct PlanView {
+  PlanHead* head;
+  int* perm;         // [M] row of the batch at sorted position p
+  int* owner;        // [M] adapter of row i of the batch, -1: none
+  int* grp_adapter;  // [G]
+  int* grp_start;    // [G] sorted positions of a group: grp_start <= p < grp_end
+  int* grp_end;      // [G]
+  int* grp_slot0;    // [G + 1] first slot
+  int* grp_tile0;    // [G + 1] first 64-row tile
+  int* adp_group;    // [n] group of an adapter, -1: no tokens
+  int* slot_group;   // [slots]
+  int* slot_tile;    // [slots] 256-row tile
+  int* tile_slot0;   // [tiles + 1] first slot of a 256-row tile
+  int* counts;       // scratch: [32][n + 1], then [n + 1] each of first, total, start
+  int M, n;
+};
+
+// Sum over the block's threads before this one, and the total (x, y apart).
+__device__ __forceinline__ int2 block_scan(int2 v, int2 (&sh)[MP_WARPS], int2& total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int2 s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, s.x, o), y = __shfl_up_sync(0xFFFFFFFFu, s.y, o);
+    if (lane >= o) s.x += x, s.y += y;
+  }
+  __syncthreads();  // sh of the scan before this one has been read
+  if (lane == 31) sh[warp] = s;
+  __syncthreads();
+  int2 before = make_int2(0, 0);
+  total = make_int2(0, 0);
+  for (int w = 0; w < MP_WARPS; ++w) {
+    if (w < warp) before.x += sh[w].x, before.y += sh[w].y;
+    total.x += sh[w].x, total.y += sh[w].y;
+  }
+  return make_int2(before.x + s.x - v.x, before.y + s.y - v.y);
+}
+
+// A stable counting sort by adapter in one block: each warp counts a contiguous
+// part of the tokens (equal adapters of a 32-token step by match), the counts
+// are summed over the warps, the groups are placed by a scan over the tokens
+// that are the first of their adapter, and each warp writes its part.  Once
+// per batch, for all layers; adapters outside 0 .. n - 1 mean none.
+__global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __restrict__ adapter, const PlanView v) {
+  __shared__ int2 sh[MP_WARPS];
+  __shared__ int moved;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int M = v.M, n = v.n, keys = n + 1;  // key n: no adapter
+  int* first = v.counts + MP_WARPS * keys;
+  int* total = first + keys;
+  int* start = total + keys;
+  for (int i = threadIdx.x; i < MP_WARPS * keys; i += MP_THREADS) v.counts[i] = 0;
+  for (int i = threadIdx.x; i < keys; i += MP_THREADS) first[i] = 0x7FFFFFFF;
+  for (int i = threadIdx.x; i < n; i += MP_THREADS) v.adp_group[i] = -1;
+  if (threadIdx.x == 0) moved = 0;
+  __syncthreads();
+  const int part = ((M + MP_THREADS - 1) / MP_THREADS) * 32;  // tokens of a warp
+  const int64_t w0 = static_cast<int64_t>(part) * warp;
+  const int64_t w1 = w0 + part < M ? w0 + part : M;
+  int* mine = v.counts + warp * keys;
+  for (int64_t b = w0; b < w1; b += 32) {
+    const int i = static_cast<int>(b) + lane;
+    const bool in = i < w1;
+    int key = -1;
+    if (in) {
+      const int a = adapter[i];
+      key = a >= 0 && a < n ? a : n;
+      v.owner[i] = key < n ? key : -1;
+    }
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    if (in && lane == __ffs(same) - 1) {
+      mine[key] += __popc(same);
+      atomicMin(first + key, i);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int key = threadIdx.x; key < keys; key += MP_THREADS) {
+    int run = 0;
+    for (int w = 0; w < MP_WARPS; ++w) {
+      const int c = v.counts[w * keys + key];
+      v.counts[w * keys + key] = run;
+      run += c;
+    }
+    total[key] = run;
+  }
+  __syncthreads();
+  int2 carry = make_int2(0, 0);  // groups and rows placed so far
+  for (int64_t b = 0; b < M; b += MP_THREADS) {
+    const int64_t i = b + threadIdx.x;
+    int key = -1;
+    if (i < M) {
+      const int a = v.owner[i];
+      key = a < 0 ? n : a;
+      if (first[key] != i) key = -1;
+    }
+    int2 sum;
+    const int2 at = block_scan(make_int2(key >= 0 && key < n ? 1 : 0, key >= 0 ? total[key] : 0), sh, sum);
+    if (key >= 0) {
+      start[key] = carry.y + at.y;
+      if (key < n) {
+        const int g = carry.x + at.x;
+        v.grp_adapter[g] = key;
+        v.grp_start[g] = start[key];
+        v.grp_end[g] = start[key] + total[key];
+        v.adp_group[key] = g;
+      }
+    }
+    carry.x += sum.x, carry.y += sum.y;
+  }
+  const int groups = carry.x;
+  __syncthreads();
+  for (int64_t b = w0; b < w1; b += 32) {
+    const int i = static_cast<int>(b) + lane;
+    const bool in = i < w1;
+    int key = -1;
+    if (in) {
+      const int a = v.owner[i];
+      key = a < 0 ? n : a;
+    }
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, key);
+    if (in) {
+      const int p = start[key] + mine[key] + __popc(same & ((1u << lane) - 1u));
+      v.perm[p] = i;
+      if (p != i) moved = 1;
+    }
+    __syncwarp();
+    if (in && lane == __ffs(same) - 1) mine[key] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  carry = make_int2(0, 0);  // slots and 64-row tiles
+  for (int b = 0; b < groups; b += MP_THREADS) {
+    const int g = b + threadIdx.x;
+    int t0 = 0;
+    int2 c = make_int2(0, 0);
+    if (g < groups) {
+      t0 = v.grp_start[g] / MP_SLOT_ROWS;
+      c.x = (v.grp_end[g] - 1) / MP_SLOT_ROWS - t0 + 1;
+      c.y = (v.grp_end[g] - v.grp_start[g] + MP_TILE - 1) / MP_TILE;
+    }
+    int2 sum;
+    const int2 at = block_scan(c, sh, sum);
+    if (g < groups) {
+      v.grp_slot0[g] = carry.x + at.x;
+      v.grp_tile0[g] = carry.y + at.y;
+      for (int k = 0; k < c.x; ++k) {
+        v.slot_group[carry.x + at.x + k] = g;
+        v.slot_tile[carry.x + at.x + k] = t0 + k;
+      }
+    }
+    carry.x += sum.x, carry.y += sum.y;
+  }
+  __syncthreads();
+  const int tiles = (M + MP_SLOT_ROWS - 1) / MP_SLOT_ROWS;
+  for (int t = threadIdx.x; t <= tiles; t += MP_THREADS) {
+    int lo = 0, hi = carry.x;  // the first slot whose tile is t or later
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (v.slot_tile[mid] < t)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    v.tile_slot0[t] = lo;
+  }
+  if (threadIdx.x == 0) {
+    v.grp_slot0[groups] = carry.x;
+    v.grp_tile0[groups] = carry.y;
+    *v.head = {groups, moved ? 0 : 1, carry.x, carry.y};
+  }
+}
+
+// Rows of X in sorted order, for batches that are not in it already.
+__global__ void __launch_bounds__(256) multi_sort_rows_kernel(const uint4* __restrict__ X, uint4* __restrict__ Xs,
+                                                              int vecs, const PlanView v) {
+  if (v.head->in_order) return;
+  const int64_t all = static_cast<int64_t>(v.M) * vecs;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < all;
+       q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t p = q / vecs;
+    Xs[q] = __ldg(X + static_cast<int64_t>(v.perm[p]) * vecs + (q - p * vecs));
+  }
+}
+
+// ====================================================================== rank-r products of the groups
+
+// D[p][j] = sum_k A[perm[p]][k] B[a][..] for 64 rows of one group and one part of
+// K: T = X L1 (kKN: the factor is [K][r]) and U = dY L2^T ([r][K]).  Each part
+// stores its own fp32 sums (pack adds them in order).  mma.sync and not
+// tcgen05: its 16-row granularity lets a group of one token cost one fragment
+// row instead of 128, rows are gathered by cp.async wherever they lie, and the
+// product reads its rows once at 2 r operations a value, so it is bound by
+// memory for r up to 64.  4-deep ring, 64 of K a stage; rows of 144 and 2 RP + 16
+// bytes keep ldmatrix free of bank conflicts.
+constexpr int MS_THREADS = 128;
+constexpr int MS_K = 64;
+constexpr int MS_PITCH = MS_K * 2 + 16;
+template <int RP, bool kKN>
+constexpr int ms_b_pitch() {
+  return kKN ? RP * 2 + 16 : MS_PITCH;
+}
+template <int RP, bool kKN>
+constexpr int ms_stage_bytes() {
+  return MP_TILE * MS_PITCH + (kKN ? MS_K : RP) * ms_b_pitch<RP, kKN>();
+}
+template <int RP>
+constexpr int ms_stages() {
+  return RP <= 64 ? 4 : 3;
+}
+
+struct ShrinkParams {
+  const uint16_t* A;   // [M][K]
+  const uint16_t* B;   // bank
+  int64_t b_stride;    // elements between two adapters
+  int64_t ldb;
+  int K, r;
+  int k_per_split;     // a multiple of 64
+  float* P;            // [splits][M][r]
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// The group of entry `at` of an ascending list of first entries (len = groups).
+__device__ __forceinline__ int plan_find(const int* first, int len, int at) {
+  int lo = 0, hi = len;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= at)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <int RP, bool kKN>
+__global__ void __launch_bounds__(MS_THREADS) multi_shrink_kernel(const ShrinkParams p, const PlanView v) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  constexpr int kStages = ms_stages<RP>();
+  constexpr int kStage = ms_stage_bytes<RP, kKN>();
+  constexpr int kBPitch = ms_b_pitch<RP, kKN>();
+  const int tile = blockIdx.x;
+  if (tile >= v.head->tiles) return;
+  const int grp = plan_find(v.grp_tile0, v.head->groups, tile);
+  const int row0 = v.grp_start[grp] + MP_TILE * (tile - v.grp_tile0[grp]);
+  const int nrow = min(MP_TILE, v.grp_end[grp] - row0);
+  const uint16_t* B = p.B + static_cast<int64_t>(v.grp_adapter[grp]) * p.b_stride;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k0 = blockIdx.y * p.k_per_split;
+  const int k1 = min(p.K, k0 + p.k_per_split);
+  const int steps = (k1 - k0) / MS_K;
+  const uint32_t base = smem_u32(smem_raw);
+  // this thread's rows of the A tile: 16 i + tid / 8, 16-byte column tid % 8
+  const uint16_t* arow[4];
+  bool aok[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = 16 * i + (threadIdx.x >> 3);
+    aok[i] = rr < nrow;
+    arow[i] = p.A + static_cast<int64_t>(v.perm[row0 + (aok[i] ? rr : 0)]) * p.K + 8 * (threadIdx.x & 7);
+  }
+  auto load = [&](int s) {
+    if (s < steps) {
+      const uint32_t st = base + (s % kStages) * kStage;
+      const int k = k0 + s * MS_K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cp_async16(st + (16 * i + (threadIdx.x >> 3)) * MS_PITCH + 16 * (threadIdx.x & 7), arow[i] + k, aok[i]);
+      const uint32_t sb = st + MP_TILE * MS_PITCH;
+      if constexpr (kKN) {
+        constexpr int kVec = RP / 8;
+#pragma unroll
+        for (int q = threadIdx.x; q < MS_K * kVec; q += MS_THREADS) {
+          const int kk = q / kVec, c = q % kVec;
+          const bool ok = 8 * c < p.r;
+          cp_async16(sb + kk * kBPitch + 16 * c, B + static_cast<int64_t>(k + kk) * p.ldb + (ok ? 8 * c : 0), ok);
+        }
+      } else {
+#pragma unroll
+        for (int q = threadIdx.x; q < RP * 8; q += MS_THREADS) {
+          const int j = q >> 3, c = q & 7;
+          const bool ok = j < p.r;
+          cp_async16(sb + j * kBPitch + 16 * c, B + static_cast<int64_t>(ok ? j : 0) * p.ldb + k + 8 * c, ok);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  float acc[RP / 8][4];
+#pragma unroll
+  for (int j = 0; j < RP / 8; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[j][c] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(s);
+  const bool live = 16 * warp < nrow;
+  for (int s = 0; s < steps; ++s) {
+    cp_async_wait<kStages - 2>();
+    __syncthreads();  // stage s has landed for all, and stage s - 1 has been read by all
+    load(s + kStages - 1);
+    if (!live) continue;
+    const uint32_t sa = base + (s % kStages) * kStage;
+    const uint32_t sb = sa + MP_TILE * MS_PITCH;
+#pragma unroll
+    for (int kk = 0; kk < MS_K; kk += 16) {
+      uint32_t a[4];
+      ldsm4(sa + (16 * warp + (lane & 15)) * MS_PITCH + (kk + 8 * (lane >> 4)) * 2, a);
+#pragma unroll
+      for (int j = 0; j < RP / 16; ++j) {
+        uint32_t b[4];
+        if constexpr (kKN)
+          ldsm4_t(sb + (kk + (lane & 15)) * kBPitch + (16 * j + 8 * (lane >> 4)) * 2, b);
+        else
+          ldsm4(sb + (16 * j + (lane & 7) + 8 * (lane >> 4)) * kBPitch + (kk + 8 * ((lane >> 3) & 1)) * 2, b);
+        mma_16816_bf16(acc[2 * j], a[0], a[1], a[2], a[3], b[0], b[1]);
+        mma_16816_bf16(acc[2 * j + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (!live) return;
+  float* out = p.P + static_cast<int64_t>(blockIdx.y) * v.M * p.r;
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    const int rr = 16 * warp + 8 * hh + (lane >> 2);
+    if (rr >= nrow) continue;
+    float* o = out + static_cast<int64_t>(row0 + rr) * p.r + 2 * (lane & 3);
+#pragma unroll
+    for (int j = 0; j < RP / 8; ++j)
+      if (8 * j < p.r) *reinterpret_cast<float2*>(o + 8 * j) = make_float2(acc[j][2 * hh], acc[j][2 * hh + 1]);
+  }
+}
+
+// Fills the slots of T (or U): the sum of the K parts in order, or a T given by
+// the caller, times the adapter's scale, as `parts` bf16 terms: two keep 16 bits
+// of the value (the W' product adds them to a sum of bf16 products), three 24
+// (the sums over tokens, whose results are fp32).  Also writes T itself in the
+// batch's order, zero for tokens without adapter.  blockIdx.x < max_slots: 64
+// rows (blockIdx.y) of a slot; above: the rows without adapter of a tile.
+struct PackJob {
+  const float* P;     // [splits][M][r], sorted rows, or null
+  const float* given; // [M][r], batch order (P null)
+  float* T;           // [M][r], batch order, or null
+  uint16_t* slots;    // [slots][256][parts * rp]
+  int splits;
+};
+
+struct PackParams {
+  PackJob job[2];
+  const float* s;   // [n]
+  int r, rp, parts;
+  int max_slots;
+};
+
+__global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, const PlanView v) {
+  const PackJob job = blockIdx.z == 0 ? p.job[0] : p.job[1];
+  const int slot = blockIdx.x;
+  if (slot >= p.max_slots) {
+    if (!job.T) return;
+    const int row0 = (slot - p.max_slots) * MP_SLOT_ROWS + 64 * blockIdx.y;
+    const int vec = p.r / 4;
+    for (int q = threadIdx.x; q < 64 * vec; q += blockDim.x) {
+      const int i = row0 + q / vec;
+      if (i < v.M && v.owner[i] < 0)
+        reinterpret_cast<float4*>(job.T + static_cast<int64_t>(i) * p.r)[q % vec] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  if (slot >= v.head->slots) return;
+  const int grp = v.slot_group[slot];
+  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp];
+  const float s = p.s[v.grp_adapter[grp]];
+  const int row0 = v.slot_tile[slot] * MP_SLOT_ROWS;
+  const int vec = p.rp / 4;
+  const int64_t part = static_cast<int64_t>(v.M) * p.r;
+  for (int q = threadIdx.x; q < 64 * vec; q += blockDim.x) {
+    const int rr = 64 * blockIdx.y + q / vec, c = 4 * (q % vec);
+    const int at = row0 + rr;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (at >= g0 && at < g1 && c < p.r) {
+      const int64_t orig = v.perm[at];
+      if (job.P) {
+        const float* src = job.P + static_cast<int64_t>(at) * p.r + c;
+        for (int k = 0; k < job.splits; ++k) {
+          const float4 f = *reinterpret_cast<const float4*>(src + k * part);
+          x[0] += f.x, x[1] += f.y, x[2] += f.z, x[3] += f.w;
+        }
+      } else {
+        const float4 f = *reinterpret_cast<const float4*>(job.given + orig * p.r + c);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      }
+      if (job.T) *reinterpret_cast<float4*>(job.T + orig * p.r + c) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] *= s;
+    }
+    uint16_t* dst = job.slots + (static_cast<int64_t>(slot) * MP_SLOT_ROWS + rr) * (p.parts * p.rp) + c;
+    for (int k = 0; k < p.parts; ++k) {
+      const uint32_t lo = pack_bf16x2(x[0], x[1]), hi = pack_bf16x2(x[2], x[3]);
+      *reinterpret_cast<uint2*>(dst + k * p.rp) = make_uint2(lo, hi);
+      const float f[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xFFFF0000u), __uint_as_float(hi << 16),
+                          __uint_as_float(hi & 0xFFFF0000u)};
+      // an infinity or a NaN is its first part alone
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = isfinite(f[j]) ? x[j] - f[j] : 0.0f;
+    }
+  }
+}
+
+// ====================================================================== W' product with the groups' terms
+
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                                 int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+struct MultiPairParams {
+  PairGemmParams g;         // k_ext_stages is not used: a tile has chunks stages per slot
+  int chunks;               // rp / 64
+  int rp, parts;
+  const uint16_t* A;        // [M][K], batch order
+  const uint16_t* Wd;       // W'^T [o][h]
+  const uint16_t* slots;
+  const uint16_t* bank;     // forward: L2 [n][r][o]; backward: L1 [n][h][r]
+  int K, r;
+};
+
+// One element from its own row and adapter alone, in fp32.
+template <bool kBwd>
+__device__ __noinline__ float multi_element(const MultiPairParams& p, const PlanView& v, int m, int n) {
+  const uint16_t* a = p.A + static_cast<int64_t>(v.perm[m]) * p.K;
+  float x = 0.0f;
+  for (int k = 0; k < p.K; ++k)
+    x = fmaf(bf16_bits_to_float(a[k]),
+             bf16_bits_to_float(p.Wd[kBwd ? static_cast<int64_t>(k) * p.g.N + n : static_cast<int64_t>(n) * p.K + k]), x);
+  const int t = m / MP_SLOT_ROWS;
+  for (int s = v.tile_slot0[t]; s < v.tile_slot0[t + 1]; ++s) {
+    const int g = v.slot_group[s];
+    if (m < v.grp_start[g] || m >= v.grp_end[g]) continue;
+    const uint16_t* row = p.slots + (static_cast<int64_t>(s) * MP_SLOT_ROWS + m % MP_SLOT_ROWS) * (p.parts * p.rp);
+    const uint16_t* b = p.bank + static_cast<int64_t>(v.grp_adapter[g]) * p.r * p.g.N;
+    float d = 0.0f;
+    for (int j = 0; j < p.r; ++j) {
+      const float w = bf16_bits_to_float(b[kBwd ? static_cast<int64_t>(n) * p.r + j : static_cast<int64_t>(j) * p.g.N + n]);
+      d = fmaf(bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]), w, d);
+    }
+    x += d;
+  }
+  return x;
+}
+
+// pair_gemm_kernel's pipeline (256 x 256 tiles on two-SM clusters, 128-deep
+// stages, two accumulators, K parts for what does not fill a round) with K
+// extended per tile: one stage for every slot of the tile and 64 ranks, A the
+// slot's [hi | mid] and B the same 64 ranks of the group's factor twice,
+// straight from the bank (the forward's L2 is an N-major operand, the
+// backward's L1 a K-major one; ranks past r are zero-filled by the 3-D map).
+// Rows are read in sorted order and written to their own place.
+template <bool kBwd>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
+    multi_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
+                      const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmAe,
+                      const __grid_constant__ CUtensorMap tmBe, const __grid_constant__ MultiPairParams mp,
+                      const __grid_constant__ PlanView v) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sA = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sB = sA + PG_STAGES * PG_OPND_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + PG_STAGES * PG_OPND_BYTES);
+  uint64_t* full = bars;                 // even CTA: TMA bytes of both CTAs (+ its producer)
+  uint64_t* empty = full + PG_STAGES;    // each CTA: the MMA's commit
+  uint64_t* tfull = empty + PG_STAGES;   // each CTA: accumulator complete
+  uint64_t* tempty = tfull + 2;          // even CTA: the 8 epilogue warps of the pair
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+
+  const PairGemmParams& p = mp.g;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(cluster_index_x());
+  const int npairs = static_cast<int>(cluster_count_x());
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int KM = p.k_main_stages;
+  const int m_tiles = p.units / p.n_tiles;
+  auto tile_of = [&](int u, int& mt, int& n0) {
+    const int band = u / (PG_BAND * m_tiles);
+    const int r = u - band * PG_BAND * m_tiles;
+    const int width = min(PG_BAND, p.n_tiles - band * PG_BAND);
+    mt = r / width;
+    n0 = (band * PG_BAND + r % width) * PG_BN;
+  };
+  const int n_parts = (p.units - p.full_units) * p.split;
+  const int n_items = p.full_units + n_parts;
+  const int nk = pair < n_items ? (n_items - 1 - pair) / npairs + 1 : 0;  // items of this pair
+  struct Item {
+    int mt, n0, kbeg, kend;
+    int slot0;  // first slot of the tile
+    int part;   // index of a split part (-1: a whole tile)
+  };
+  auto item_of = [&](int k) -> Item {
+    const int u = pair + k * npairs;
+    Item it;
+    it.part = u >= n_parts ? -1 : u;
+    tile_of(u >= n_parts ? u - n_parts : p.full_units + u / p.split, it.mt, it.n0);
+    it.slot0 = v.tile_slot0[it.mt];
+    const int S = KM + (v.tile_slot0[it.mt + 1] - it.slot0) * mp.chunks;
+    it.kbeg = 0;
+    it.kend = S;
+    if (it.part >= 0) {
+      const int64_t j = u % p.split;
+      it.kbeg = static_cast<int>(j * S / p.split);
+      it.kend = static_cast<int>((j + 1) * S / p.split);
+    }
+    return it;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PG_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 8);
+    }
+    fence_mbar_init();
+    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmAe);
+    tma_prefetch_map(&tmBe);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 2 * PG_ACC_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_barrier();  // both CTAs' barriers initialised and TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer: this CTA's 128 rows of A and of B of a stage
+      const CUtensorMap* ma = v.head->in_order ? &tmA : &tmAs;
+      int G = 0;
+      bool ok = true;
+      for (int k = 0; k < nk && ok; ++k) {
+        const Item it = item_of(k);
+        const int m0 = it.mt * PG_BM + static_cast<int>(rank) * 128;
+        const int n0 = it.n0 + static_cast<int>(rank) * 128;
+        for (int i = it.kbeg; i < it.kend; ++i, ++G) {
+          const int s = G % PG_STAGES;
+          if (!mbar_wait_idle(&empty[s], ((G / PG_STAGES) & 1) ^ 1, kTagPgEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = cluster_addr(&full[s], 0);
+          uint8_t* a_dst = sA + s * PG_OPND_BYTES;
+          uint8_t* b_dst = sB + s * PG_OPND_BYTES;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 4 * PG_OPND_BYTES);
+          if (i < KM) {
+            const int k0 = i * PG_BK;
+            tma_load_2d_pair(a_dst, ma, fb, k0, m0);
+            tma_load_2d_pair(a_dst + PG_ATOM_BYTES, ma, fb, k0 + 64, m0);
+            if (kBwd) {
+              tma_load_2d_pair(b_dst, &tmB, fb, n0, k0);
+              tma_load_2d_pair(b_dst + PG_ATOM_BYTES, &tmB, fb, n0 + 64, k0);
+            } else {
+              tma_load_2d_pair(b_dst, &tmB, fb, k0, n0);
+              tma_load_2d_pair(b_dst + PG_ATOM_BYTES, &tmB, fb, k0 + 64, n0);
+            }
+          } else {
+            const int e = (i - KM) / mp.chunks;
+            const int x = ((i - KM) - e * mp.chunks) * 64;
+            const int slot = it.slot0 + e;
+            const int a = v.grp_adapter[v.slot_group[slot]];
+            const int y = slot * MP_SLOT_ROWS + static_cast<int>(rank) * 128;
+            tma_load_2d_pair(a_dst, &tmAe, fb, x, y);
+            tma_load_2d_pair(a_dst + PG_ATOM_BYTES, &tmAe, fb, mp.rp + x, y);
+            if (kBwd) {
+              // K-major: 64 ranks of 128 rows of L1, once for each half of the stage
+              tma_load_3d_pair(b_dst, &tmBe, fb, x, n0, a);
+              tma_load_3d_pair(b_dst + PG_ATOM_BYTES, &tmBe, fb, x, n0, a);
+            } else {
+              // N-major: per 64 columns of L2 its 64 ranks twice, one below the other
+              for (int h = 0; h < 2; ++h)
+                for (int c = 0; c < 2; ++c)
+                  tma_load_3d_pair(b_dst + c * PG_ATOM_BYTES + h * (PG_ATOM_BYTES / 2), &tmBe, fb, n0 + 64 * c, x, a);
+            }
+          }
+        }
+      }
+      // Leave no copy in flight: the even CTA's last phases count both CTAs' bytes.
+      if (rank == 0)
+        for (int g = G - PG_STAGES > 0 ? G - PG_STAGES : 0; g < G; ++g)
+          mbar_wait_idle(&full[g % PG_STAGES], (g / PG_STAGES) & 1, kTagPgFull);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ---------------- MMA issuer (even CTA)
+      uint64_t a_desc0[PG_STAGES], b_desc0[PG_STAGES], bmn_desc0[PG_STAGES];
+#pragma unroll
+      for (int s = 0; s < PG_STAGES; ++s) {
+        a_desc0[s] = sw128_desc(smem_u32(sA + s * PG_OPND_BYTES), 16, 1024);
+        b_desc0[s] = sw128_desc(smem_u32(sB + s * PG_OPND_BYTES), 16, 1024);
+        bmn_desc0[s] = sw128_desc(smem_u32(sB + s * PG_OPND_BYTES), PG_ATOM_BYTES, 1024);
+      }
+      int G = 0;
+      bool ok = true;
+      for (int k = 0; k < nk && ok; ++k) {
+        const int b = k & 1;
+        if (!mbar_wait_idle<true>(&tempty[b], ((k >> 1) & 1) ^ 1, kTagPgTEmpty)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + static_cast<uint32_t>(b * PG_ACC_COLS);
+        const Item it = item_of(k);
+        for (int i = it.kbeg; i < it.kend; ++i, ++G) {
+          const int s = G % PG_STAGES;
+          if (!mbar_wait(&full[s], (G / PG_STAGES) & 1, kTagPgFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool b_mn = kBwd == (i < KM);
+          const uint64_t ad = s == 0 ? a_desc0[0] : (s == 1 ? a_desc0[1] : a_desc0[2]);
+          const uint64_t bd = b_mn ? (s == 0 ? bmn_desc0[0] : (s == 1 ? bmn_desc0[1] : bmn_desc0[2]))
+                                   : (s == 0 ? b_desc0[0] : (s == 1 ? b_desc0[1] : b_desc0[2]));
+          const uint32_t idesc = idesc_bf16(PG_BM, PG_BN, false, false) | (b_mn ? 1u << 16 : 0u);
+#pragma unroll
+          for (int kk = 0; kk < PG_BK / 16; ++kk) {
+            const uint32_t k_off = ((kk >> 2) * PG_ATOM_BYTES + (kk & 3) * 32) >> 4;
+            const uint64_t adesc = ad + k_off;
+            const uint64_t bdesc = bd + (b_mn ? static_cast<uint32_t>(kk * 2048 >> 4) : k_off);
+            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (i > it.kbeg || kk > 0) ? 1u : 0u);
+          }
+          umma_commit_pair(&empty[s], 0x3);
+        }
+        if (ok) umma_commit_pair(&tfull[b], 0x3);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---------------- epilogue: warp q drains TMEM lanes 32 q .. 32 q + 31 (this CTA's rows)
+    const int q = warp & 3;
+    auto store_row = [&](int m, int64_t row, int n, float* x, bool shared) {
+      if (m >= p.M || n >= p.N) return;
+      if (shared) {
+        // x 0 is 0 for finite x: one fused multiply-add each finds what is not
+        float z = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) z = fmaf(x[t], 0.0f, z);
+        if (z != 0.0f)
+          for (int t = 0; t < 16; ++t) {
+            float y = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) y = u == t ? x[u] : y;
+            if (isfinite(y)) continue;
+            y = multi_element<kBwd>(mp, v, m, n + t);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) x[u] = u == t ? y : x[u];
+          }
+      }
+      if (p.out_bf16) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.ld_out + n);
+        uint32_t h[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) h[t] = pack_bf16x2(x[2 * t], x[2 * t + 1]);
+        __stcs(dst, make_uint4(h[0], h[1], h[2], h[3]));
+        __stcs(dst + 1, make_uint4(h[4], h[5], h[6], h[7]));
+      } else {
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.ld_out + n);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) __stcs(dst + t, make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]));
+      }
+    };
+    for (int k = 0; k < nk; ++k) {
+      const int b = k & 1;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_idle(&tfull[b], (k >> 1) & 1, kTagPgTFull))) break;
+      tc_fence_after();
+      const Item it = item_of(k);
+      const int row = static_cast<int>(rank) * 128 + q * 32 + lane;  // row within the pair tile
+      const int m = it.mt * PG_BM + row;
+      const int64_t to = m < p.M ? v.perm[m] : 0;
+      // whether rows of several owners (groups, or none) meet in the tile
+      const int ns = v.tile_slot0[it.mt + 1] - it.slot0;
+      bool shared = ns > 1;
+      if (ns == 1) {
+        const int g = v.slot_group[it.slot0];
+        shared = v.grp_start[g] > it.mt * PG_BM || v.grp_end[g] < min((it.mt + 1) * PG_BM, p.M);
+      }
+      float* part = it.part >= 0 ? p.partial + (static_cast<int64_t>(it.part) * PG_BM + row) * PG_BN : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < PG_ACC_COLS / 16; ++c) {
+        uint32_t r[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * PG_ACC_COLS + c * 16), r);
+        tmem_ld_wait();
+        if (c == PG_ACC_COLS / 16 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_even(&tempty[b], rank);
+        }
+        float x[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(r[t]);
+        if (part) {
+          float4* dst = reinterpret_cast<float4*>(part + c * 16);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
+        } else {
+          store_row(m, to, it.n0 + c * 16, x, shared);
+        }
+      }
+      if (part) {
+        // the warp that completes the last part of a tile sums the parts in order
+        __threadfence();
+        __syncwarp();
+        const int tail = it.part / p.split;
+        unsigned prior = 0;
+        if (lane == 0) prior = atomicAdd(&p.counters[(tail * 2 + static_cast<int>(rank)) * 4 + q], 1u);
+        prior = __shfl_sync(0xFFFFFFFFu, prior, 0);
+        if (prior == static_cast<unsigned>(p.split - 1)) {
+          __threadfence();
+          const float* first = p.partial + (static_cast<int64_t>(tail) * p.split * PG_BM + row) * PG_BN;
+#pragma unroll 1
+          for (int c = 0; c < PG_ACC_COLS / 16; ++c) {
+            float x[16];
+#pragma unroll
+            for (int t = 0; t < 16; ++t) x[t] = 0.0f;
+            for (int j = 0; j < p.split; ++j) {
+              const float4* src = reinterpret_cast<const float4*>(first + static_cast<int64_t>(j) * PG_BM * PG_BN + c * 16);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const float4 a = __ldcg(src + t);
+                x[4 * t] += a.x;
+                x[4 * t + 1] += a.y;
+                x[4 * t + 2] += a.z;
+                x[4 * t + 3] += a.w;
+              }
+            }
+            store_row(m, to, it.n0 + c * 16, x, shared);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_barrier();  // no CTA leaves while the other may still touch its barriers or TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * PG_ACC_COLS);
+  }
+}
+
+// ====================================================================== gradients of the factors
+
+// dL1[a] = X_a^T (s U_a) and dL2[a]^T = dY_a^T (s T_a) over the rows of group a:
+// D is 128 rows of h (or o) by the ranks, K runs over the group's 64-row blocks
+// of the sorted order, A from X (or dY) as it lies (M-major), B the slots' three
+// bf16 parts (N-major), three MMAs a step into one accumulator.  The slots are
+// zero in the rows of a block that belong to others.  One CTA adds all tokens of
+// its tile in order and stores them, so the gradients do not depend on timing;
+// adapters without tokens get zeros.  blockIdx.x: tiles of dL1, then of dL2;
+// blockIdx.y: adapter.
+constexpr int MD_BM = 128;
+constexpr int MD_BK = 64;
+constexpr int MD_THREADS = 128;
+constexpr int MD_A_BYTES = MD_BM * MD_BK * 2;
+constexpr int MD_MAX_STAGES = 4;
+constexpr int MD_SMEM_LIMIT = 110 * 1024;  // two CTAs an SM
+constexpr int MD_PARTS = 3;
+
+struct MultiGradSide {
+  const uint16_t* A;      // X or dY, batch order
+  const uint16_t* slots;  // of U or T
+  float* out;             // dL1 [n][h][r] or dL2 [n][r][o]
+  int rows;               // h or o
+};
+
+struct MultiGradParams {
+  MultiGradSide side[2];
+  int r, rp, bn, stages;
+  int tiles0;  // 128-row tiles of dL1, times the rank tiles
+};
+
+__global__ void __launch_bounds__(MD_THREADS, 1)
+    multi_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
+                      const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDs,
+                      const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmT,
+                      const __grid_constant__ MultiGradParams p, const __grid_constant__ PlanView v) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int b_bytes = p.bn * MD_BK * 2;
+  const int stage_bytes = MD_A_BYTES + MD_PARTS * b_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
+  uint64_t* empty = full + MD_MAX_STAGES;
+  uint64_t* accum = empty + MD_MAX_STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int second = static_cast<int>(blockIdx.x) >= p.tiles0 ? 1 : 0;
+  const MultiGradSide side = second ? p.side[1] : p.side[0];
+  const int n_tiles = p.rp / p.bn;
+  const int tile = static_cast<int>(blockIdx.x) - (second ? p.tiles0 : 0);
+  const int m0 = (tile / n_tiles) * MD_BM;
+  const int j0 = (tile % n_tiles) * p.bn;
+  const int adapter = blockIdx.y;
+  const int grp = v.adp_group[adapter];
+  float* out = side.out + static_cast<int64_t>(adapter) * p.r * side.rows;
+  const int m = m0 + threadIdx.x;
+  auto store = [&](int n, const float* x) {  // 16 ranks n .. n + 15 of row m
+    if (m >= side.rows) return;
+#pragma unroll
+    for (int t = 0; t < 16; t += 4) {
+      if (n + t >= p.r) return;
+      if (second) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) out[static_cast<int64_t>(n + t + u) * side.rows + m] = x[t + u];
+      } else {
+        *reinterpret_cast<float4*>(out + static_cast<int64_t>(m) * p.r + n + t) =
+            make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
+      }
+    }
+  };
+  if (grp < 0) {
+    const float zero[16] = {};
+    for (int c = 0; c < p.bn; c += 16) store(j0 + c, zero);
+    return;
+  }
+  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp];
+  const int blk0 = g0 / MD_BK;
+  const int S = (g1 - 1) / MD_BK - blk0 + 1;
+  const int slot0 = v.grp_slot0[grp];
+  const uint32_t tmem_cols = p.bn <= 64 ? 64u : 128u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(accum, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    const CUtensorMap* ma = second ? (v.head->in_order ? &tmD : &tmDs) : (v.head->in_order ? &tmX : &tmXs);
+    const CUtensorMap* mb = second ? &tmT : &tmU;
+    int issued = 0;
+    for (int i = 0; i < S; ++i) {
+      const int s = i % p.stages;
+      if (!mbar_wait(&empty[s], ((i / p.stages) & 1) ^ 1)) break;
+      uint8_t* st = smem + s * stage_bytes;
+      const int row = (blk0 + i) * MD_BK;
+      // the block's rows within the group's slots
+      const int y = (slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
+      mbar_arrive_expect_tx(&full[s], stage_bytes);
+      tma_load_2d(st, ma, &full[s], m0, row);
+      tma_load_2d(st + MD_A_BYTES / 2, ma, &full[s], m0 + 64, row);
+      for (int h = 0; h < MD_PARTS; ++h)
+        for (int t = 0; t < p.bn / 64; ++t)
+          tma_load_2d(st + MD_A_BYTES + h * b_bytes + t * 8192, mb, &full[s], h * p.rp + j0 + 64 * t, y);
+      issued = i + 1;
+    }
+    for (int i = issued - p.stages > 0 ? issued - p.stages : 0; i < issued; ++i)
+      mbar_wait(&full[i % p.stages], (i / p.stages) & 1);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(MD_BM, p.bn, true, true);
+    for (int i = 0; i < S; ++i) {
+      const int s = i % p.stages;
+      if (!mbar_wait(&full[s], (i / p.stages) & 1)) break;
+      tc_fence_after();
+      const uint32_t a_base = smem_u32(smem + s * stage_bytes);
+#pragma unroll
+      for (int kk = 0; kk < MD_BK / 16; ++kk) {
+        const uint64_t adesc = sw128_desc(a_base + kk * 2048, MD_A_BYTES / 2, 1024);
+#pragma unroll
+        for (int h = 0; h < MD_PARTS; ++h) {
+          const uint64_t bdesc = sw128_desc(a_base + MD_A_BYTES + h * b_bytes + kk * 2048, 8192, 1024);
+          umma_bf16(tmem, adesc, bdesc, idesc, (i > 0 || kk > 0 || h > 0) ? 1u : 0u);
+        }
+      }
+      umma_commit(&empty[s]);
+    }
+    umma_commit(accum);
+  }
+
+  __syncwarp();
+  const bool ok = mbar_wait(accum, 0);
+  tc_fence_after();
+  if (ok) {
+    // rows of others in the group's first or last block
+    const bool shared = g0 % MD_BK != 0 || (g1 % MD_BK != 0 && g1 < v.M);
+    for (int c = 0; c < p.bn; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
+      tmem_ld_wait();
+      float x[16];
+      float z = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        x[t] = __uint_as_float(r[t]);
+        z = fmaf(x[t], 0.0f, z);
+      }
+      if (shared && z != 0.0f && m < side.rows) {
+        for (int t = 0; t < 16; ++t) {
+          if (j0 + c + t >= p.r) break;
+          float y = 0.0f;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) y = u == t ? x[u] : y;
+          if (isfinite(y)) continue;
+          y = 0.0f;
+          for (int row = g0; row < g1; ++row) {
+            const uint16_t* b = side.slots + (static_cast<int64_t>(slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) *
+                                                  MP_SLOT_ROWS + row % MP_SLOT_ROWS) * (MD_PARTS * p.rp) + j0 + c + t;
+            const float w = bf16_bits_to_float(b[0]) + bf16_bits_to_float(b[p.rp]) + bf16_bits_to_float(b[2 * p.rp]);
+            y = fmaf(bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]), w, y);
+          }
+#pragma unroll
+          for (int u = 0; u < 16; ++u) x[u] = u == t ? y : x[u];
+        }
+      }
+      store(j0 + c, x);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+}  // namespace qlora

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "gemm.cuh"
+#include "multi.cuh"
 #include "optim.cuh"
 #include "pairgemm.cuh"
 #include "quant.cuh"
@@ -1451,6 +1452,382 @@ const char* qlora_kernel_family_name(int family) {
 }
 
 int64_t qlora_launch_count(void) { return g_launches.load(); }
+
+}  // extern "C"
+
+// ====================================================================== many adapters beside one weight
+
+namespace {
+
+constexpr int kMaxAdapters = 65535;
+constexpr int64_t kMaxPlanTokens = int64_t(1) << 28;
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Slots of a batch: a 256-row tile has one, and one more for every group that begins inside it.
+int64_t max_slots(int64_t M, int n) { return div_up(M, MP_SLOT_ROWS) + (n < M ? n : M); }
+
+size_t plan_layout(void* base, int64_t M, int n, PlanView* v) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](int64_t ints) -> int* {
+    int* q = p ? reinterpret_cast<int*>(p + off) : nullptr;
+    off += round256(static_cast<size_t>(ints) * 4);
+    return q;
+  };
+  const int64_t g = n < M ? n : M, slots = max_slots(M, n), keys = static_cast<int64_t>(n) + 1;
+  PlanView w{};
+  w.head = reinterpret_cast<PlanHead*>(take(4));
+  w.perm = take(M);
+  w.owner = take(M);
+  w.grp_adapter = take(g);
+  w.grp_start = take(g);
+  w.grp_end = take(g);
+  w.grp_slot0 = take(g + 1);
+  w.grp_tile0 = take(g + 1);
+  w.adp_group = take(n);
+  w.slot_group = take(slots);
+  w.slot_tile = take(slots);
+  w.tile_slot0 = take(div_up(M, MP_SLOT_ROWS) + 1);
+  w.counts = take((MP_WARPS + 3) * keys);
+  w.M = static_cast<int>(M);
+  w.n = n;
+  if (v) *v = w;
+  return off;
+}
+
+int check_plan_args(int64_t M, int n) {
+  if (M < 1 || M > kMaxPlanTokens) return QLORA_ERR_SHAPE;
+  return n < 1 || n > kMaxAdapters ? QLORA_ERR_UNSUPPORTED : QLORA_OK;
+}
+
+int rank_pad(int r) { return ((r + 63) / 64) * 64; }
+
+// K parts of a rank-r product: enough blocks for about three an SM, each at least 256 deep.
+int shrink_splits(int64_t M, int n, int64_t K) {
+  const int64_t tiles = div_up(M, MP_TILE) + (n < M ? n : M) - 1;
+  int64_t s = 3 * sm_count() / tiles;
+  if (s > K / 256) s = K / 256;
+  if (s < 1) s = 1;
+  const int64_t per = div_up(K / MS_K, s);
+  return static_cast<int>(div_up(K / MS_K, per));
+}
+
+struct MultiWs {
+  uint16_t* Xs;    // [M][h] rows of X in sorted order
+  uint16_t* Ds;    // [M][o] rows of dY in sorted order (backward)
+  float* PT;       // parts of T (backward: only when T is recomputed)
+  float* PU;       // parts of U (backward)
+  uint16_t* ST;    // slots of T
+  uint16_t* SU;    // slots of U (backward)
+  uint16_t* Wd;    // W'^T
+  float* Wpart;
+  unsigned* Wcnt;
+  size_t bytes;
+};
+
+MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int r, bool bwd) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](int64_t bytes) -> void* {
+    void* q = p ? p + off : nullptr;
+    off += round256(static_cast<size_t>(bytes));
+    return q;
+  };
+  const int64_t pairs = (sm_count() + 1) / 2;
+  const int64_t slot_bytes = max_slots(M, n) * MP_SLOT_ROWS * rank_pad(r) * (bwd ? 3 : 2) * 2;
+  MultiWs w{};
+  w.Xs = static_cast<uint16_t*>(take(M * h * 2));
+  w.PT = static_cast<float*>(take(shrink_splits(M, n, h) * M * r * 4));
+  w.ST = static_cast<uint16_t*>(take(slot_bytes));
+  if (bwd) {
+    w.Ds = static_cast<uint16_t*>(take(M * o * 2));
+    w.PU = static_cast<float*>(take(shrink_splits(M, n, o) * M * r * 4));
+    w.SU = static_cast<uint16_t*>(take(slot_bytes));
+  }
+  w.Wd = static_cast<uint16_t*>(take(o * h * 2));
+  w.Wpart = static_cast<float*>(take(pairs * PG_BM * PG_BN * 4));
+  w.Wcnt = static_cast<unsigned*>(take(pairs * 8 * 4));
+  w.bytes = off;
+  return w;
+}
+
+int sort_rows(const void* X, uint16_t* Xs, int64_t width, const PlanView& v, cudaStream_t st) {
+  LaunchScope ls(QLORA_KERNEL_AUX, st);
+  const int vecs = static_cast<int>(width / 8);
+  multi_sort_rows_kernel<<<static_cast<unsigned>(grid_for(static_cast<int64_t>(v.M) * vecs, 1024, sm_count() * 8)), 256,
+                           0, st>>>(static_cast<const uint4*>(X), reinterpret_cast<uint4*>(Xs), vecs, v);
+  return launch_status();
+}
+
+template <int RP, bool kKN>
+int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, cudaStream_t st) {
+  const int smem = ms_stages<RP>() * ms_stage_bytes<RP, kKN>();
+  if (set_smem(multi_shrink_kernel<RP, kKN>, smem) != QLORA_OK) return QLORA_ERR_CUDA;
+  const int64_t tiles = div_up(v.M, MP_TILE) + (v.n < v.M ? v.n : v.M);
+  {
+    LaunchScope ls(QLORA_KERNEL_TGEMM, st);
+    multi_shrink_kernel<RP, kKN><<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits)), MS_THREADS, smem,
+                                   st>>>(p, v);
+  }
+  return launch_status();
+}
+
+// Parts of A B[a] of every group: A [M][K]; kKN: B [n][K][r], else [n][r][K].
+template <bool kKN>
+int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, cudaStream_t st) {
+  const int splits = shrink_splits(v.M, v.n, K);
+  ShrinkParams p{};
+  p.A = static_cast<const uint16_t*>(A);
+  p.B = static_cast<const uint16_t*>(B);
+  p.b_stride = K * r;
+  p.ldb = kKN ? r : K;
+  p.K = static_cast<int>(K);
+  p.r = r;
+  p.k_per_split = static_cast<int>(div_up(K / MS_K, splits)) * MS_K;
+  p.P = P;
+  if (r <= 16) return launch_shrink_as<16, kKN>(p, splits, v, st);
+  if (r <= 32) return launch_shrink_as<32, kKN>(p, splits, v, st);
+  if (r <= 64) return launch_shrink_as<64, kKN>(p, splits, v, st);
+  if (r <= 128) return launch_shrink_as<128, kKN>(p, splits, v, st);
+  return launch_shrink_as<256, kKN>(p, splits, v, st);
+}
+
+int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int parts, const PlanView& v,
+                cudaStream_t st) {
+  PackParams p{};
+  p.job[0] = j0;
+  if (j1) p.job[1] = *j1;
+  p.s = s;
+  p.r = r;
+  p.rp = rank_pad(r);
+  p.parts = parts;
+  p.max_slots = static_cast<int>(max_slots(v.M, v.n));
+  const int64_t x = p.max_slots + div_up(v.M, MP_SLOT_ROWS);
+  {
+    LaunchScope ls(QLORA_KERNEL_AUX, st);
+    multi_pack_kernel<<<dim3(static_cast<unsigned>(x), MP_SLOT_ROWS / 64, j1 ? 2 : 1), 256, 0, st>>>(p, v);
+  }
+  return launch_status();
+}
+
+template <bool kBwd>
+int multi_resident_pairs() {
+  static std::atomic<int> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cache[dev].load();
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>((sm_count() + 1) / 2), 1, 1);
+  cfg.blockDim = dim3(PG_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = PG_SMEM_BYTES;
+  if (cudaOccupancyMaxActiveClusters(&n, multi_pair_kernel<kBwd>, &cfg) != cudaSuccess || n <= 0) return 0;
+  cache[dev].store(n);
+  return n;
+}
+
+// out = A (op W') + the groups' terms.  A [M][K] in batch order, As its sorted copy.
+template <bool kBwd>
+int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, const qlora_adapters_t* ad,
+                      const uint16_t* Wd, int64_t o, int64_t h, int parts, void* out, int out_bf16, const MultiWs& w,
+                      const PlanView& v, cudaStream_t st) {
+  const int64_t M = v.M, K = kBwd ? o : h, N = kBwd ? h : o;
+  const int64_t r = ad->r, rp = rank_pad(ad->r), rows = max_slots(M, v.n) * MP_SLOT_ROWS;
+  CUtensorMap ma, mas, mb, mae, mbe;
+  if (!map_bf16(&ma, A, K, M, K * 2, 64, 128) || !map_bf16(&mas, As, K, M, K * 2, 64, 128) ||
+      !map_bf16(&mb, Wd, h, o, h * 2, 64, 128) || !map_bf16(&mae, slots, parts * rp, rows, parts * rp * 2, 64, 128))
+    return QLORA_ERR_CUDA;
+  if (kBwd ? !map_bf16_3d(&mbe, ad->L1, r, h, ad->n, r * 2, h * r * 2, 64, 128, 1)
+           : !map_bf16_3d(&mbe, ad->L2, o, r, ad->n, o * 2, r * o * 2, 64, 64, 1))
+    return QLORA_ERR_CUDA;
+  if (set_smem(multi_pair_kernel<kBwd>, PG_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+  int pairs = multi_resident_pairs<kBwd>();
+  if (pairs <= 0) return QLORA_ERR_CUDA;
+  if (pairs > (sm_count() + 1) / 2) pairs = (sm_count() + 1) / 2;  // the partial buffer's bound
+  MultiPairParams p{};
+  p.g.M = static_cast<int>(M);
+  p.g.N = static_cast<int>(N);
+  p.g.k_main_stages = static_cast<int>(div_up(K, PG_BK));
+  p.g.n_tiles = static_cast<int>(div_up(N, PG_BN));
+  p.g.units = static_cast<int>(div_up(M, PG_BM)) * p.g.n_tiles;
+  p.g.out = out;
+  p.g.out_bf16 = out_bf16;
+  p.g.ld_out = N;
+  // The tiles of the last round, which would leave pairs without work, are split along K, each
+  // part at least two stages deep; up to four parts a tile beside whole tiles, up to eight when
+  // there are none (a batch of a few tokens).
+  const int tail = p.g.units % pairs;
+  const int most = p.g.units < pairs ? 8 : 4;
+  int split = tail > 0 ? pairs / tail : 1;
+  if (split > most) split = most;
+  if (split > p.g.k_main_stages / 2) split = p.g.k_main_stages / 2;
+  if (split < 2) split = 1;
+  p.g.split = split;
+  p.g.full_units = split > 1 ? p.g.units - tail : p.g.units;
+  p.g.partial = w.Wpart;
+  p.g.counters = w.Wcnt;
+  p.chunks = static_cast<int>(rp / 64);
+  p.rp = static_cast<int>(rp);
+  p.parts = parts;
+  p.A = static_cast<const uint16_t*>(A);
+  p.Wd = Wd;
+  p.slots = slots;
+  p.bank = static_cast<const uint16_t*>(kBwd ? ad->L1 : ad->L2);
+  p.K = static_cast<int>(K);
+  p.r = ad->r;
+  if (split > 1 && cudaMemsetAsync(w.Wcnt, 0, static_cast<size_t>(tail) * 8 * 4, st) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  const int items = p.g.full_units + (p.g.units - p.g.full_units) * split;
+  const int clusters = items < pairs ? items : pairs;
+  {
+    LaunchScope ls(kBwd ? QLORA_KERNEL_FUSED_BWD : QLORA_KERNEL_FUSED_FWD, st);
+    multi_pair_kernel<kBwd><<<2 * clusters, PG_THREADS, PG_SMEM_BYTES, st>>>(ma, mas, mb, mae, mbe, p, v);
+  }
+  return launch_status();
+}
+
+int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlora_adapters_t* ad, int64_t o,
+                      int64_t h, float* dL1, float* dL2, const PlanView& v, cudaStream_t st) {
+  const int64_t M = v.M, rp = rank_pad(ad->r), width = MD_PARTS * rp, rows = max_slots(M, v.n) * MP_SLOT_ROWS;
+  CUtensorMap mx, mxs, md, mds, mu, mt;
+  if (!map_bf16(&mx, X, h, M, h * 2, 64, 64) || !map_bf16(&mxs, w.Xs, h, M, h * 2, 64, 64) ||
+      !map_bf16(&md, dY, o, M, o * 2, 64, 64) || !map_bf16(&mds, w.Ds, o, M, o * 2, 64, 64) ||
+      !map_bf16(&mu, w.SU, width, rows, width * 2, 64, 64) || !map_bf16(&mt, w.ST, width, rows, width * 2, 64, 64))
+    return QLORA_ERR_CUDA;
+  MultiGradParams p{};
+  p.side[0] = {static_cast<const uint16_t*>(X), w.SU, dL1, static_cast<int>(h)};
+  p.side[1] = {static_cast<const uint16_t*>(dY), w.ST, dL2, static_cast<int>(o)};
+  p.r = ad->r;
+  p.rp = static_cast<int>(rp);
+  p.bn = rp % 128 == 0 ? 128 : 64;
+  const int stage_bytes = MD_A_BYTES + MD_PARTS * p.bn * MD_BK * 2;
+  p.stages = MD_SMEM_LIMIT / stage_bytes;
+  if (p.stages < 2) p.stages = TG_SMEM_LIMIT_ONE / stage_bytes;
+  if (p.stages > MD_MAX_STAGES) p.stages = MD_MAX_STAGES;
+  const int n_tiles = p.rp / p.bn;
+  p.tiles0 = static_cast<int>(div_up(h, MD_BM)) * n_tiles;
+  const int tiles = p.tiles0 + static_cast<int>(div_up(o, MD_BM)) * n_tiles;
+  const int smem = p.stages * stage_bytes + 1024 + 256;
+  if (set_smem(multi_grad_kernel, smem) != QLORA_OK) return QLORA_ERR_CUDA;
+  {
+    LaunchScope ls(QLORA_KERNEL_TGEMM, st);
+    multi_grad_kernel<<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ad->n)), MD_THREADS, smem, st>>>(
+        mx, mxs, md, mds, mu, mt, p, v);
+  }
+  return launch_status();
+}
+
+int check_multi_args(const qlora_nf4_t* Wq, int64_t M, const qlora_adapters_t* ad, int dtype, const void* plan,
+                     size_t plan_bytes) {
+  if (!ad) return QLORA_ERR_NULL;
+  int rc = check_linear_args(Wq, M, ad->r, dtype);
+  if (rc != QLORA_OK) return rc;
+  rc = check_plan_args(M, ad->n);
+  if (rc != QLORA_OK) return rc;
+  if (!ad->L1 || !ad->L2 || !ad->s || !plan) return QLORA_ERR_NULL;
+  if (!aligned16(ad->L1) || !aligned16(ad->L2) || (reinterpret_cast<uintptr_t>(ad->s) & 3u) || !aligned16(plan))
+    return QLORA_ERR_ALIGN;
+  return plan_bytes < plan_layout(nullptr, M, ad->n, nullptr) ? QLORA_ERR_WORKSPACE : QLORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_adapter_plan_size(int64_t M, int n) {
+  return check_plan_args(M, n) == QLORA_OK ? plan_layout(nullptr, M, n, nullptr) : 0;
+}
+
+int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, size_t plan_bytes, void* stream) {
+  const int rc = check_plan_args(M, n);
+  if (rc != QLORA_OK) return rc;
+  if (!adapter) return QLORA_ERR_NULL;
+  if (!plan || plan_bytes < plan_layout(nullptr, M, n, nullptr)) return QLORA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(adapter) & 3u) || !aligned16(plan)) return QLORA_ERR_ALIGN;
+  PlanView v;
+  plan_layout(plan, M, n, &v);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    LaunchScope ls(QLORA_KERNEL_AUX, st);
+    adapter_plan_kernel<<<1, MP_THREADS, 0, st>>>(adapter, v);
+  }
+  return launch_status();
+}
+
+size_t qlora_multi_linear_fwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r) {
+  return multi_ws_layout(nullptr, o, h, M, n, r, false).bytes;
+}
+
+size_t qlora_multi_linear_bwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r) {
+  return multi_ws_layout(nullptr, o, h, M, n, r, true).bytes;
+}
+
+int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, const qlora_adapters_t* ad,
+                           const void* plan, size_t plan_bytes, void* Y, int y_dtype, float* T_save, void* ws,
+                           size_t ws_bytes, void* stream) {
+  int rc = check_multi_args(Wq, M, ad, y_dtype, plan, plan_bytes);
+  if (rc != QLORA_OK) return rc;
+  if (!X || !Y) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(T_save) || !aligned16(ws)) return QLORA_ERR_ALIGN;
+  const int64_t o = Wq->o, h = Wq->h;
+  const int r = ad->r;
+  if (!ws || ws_bytes < multi_ws_layout(nullptr, o, h, M, ad->n, r, false).bytes) return QLORA_ERR_WORKSPACE;
+  const MultiWs w = multi_ws_layout(ws, o, h, M, ad->n, r, false);
+  PlanView v;
+  plan_layout(const_cast<void*>(plan), M, ad->n, &v);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (sort_rows(X, w.Xs, h, v, st) != QLORA_OK) return QLORA_ERR_CUDA;
+  rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st);
+  if (rc != QLORA_OK) return rc;
+  PackJob j{};
+  j.P = w.PT;
+  j.T = T_save;
+  j.slots = w.ST;
+  j.splits = shrink_splits(M, ad->n, h);
+  rc = launch_pack(j, nullptr, ad->s, r, 2, v, st);
+  if (rc != QLORA_OK) return rc;
+  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
+  if (rc != QLORA_OK) return rc;
+  return launch_multi_pair<false>(X, w.Xs, w.ST, ad, w.Wd, o, h, 2, Y, y_dtype == QLORA_DTYPE_BF16, w, v, st);
+}
+
+int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY, int64_t M,
+                           const qlora_adapters_t* ad, const void* plan, size_t plan_bytes, const float* T_saved,
+                           void* dX, int dx_dtype, float* dL1, float* dL2, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_multi_args(Wq, M, ad, dx_dtype, plan, plan_bytes);
+  if (rc != QLORA_OK) return rc;
+  if (!X || !dY || !dX || !dL1 || !dL2) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(dY) || !aligned16(dX) || !aligned16(dL1) || !aligned16(dL2) ||
+      !aligned16(T_saved) || !aligned16(ws))
+    return QLORA_ERR_ALIGN;
+  const int64_t o = Wq->o, h = Wq->h;
+  const int r = ad->r;
+  if (!ws || ws_bytes < multi_ws_layout(nullptr, o, h, M, ad->n, r, true).bytes) return QLORA_ERR_WORKSPACE;
+  const MultiWs w = multi_ws_layout(ws, o, h, M, ad->n, r, true);
+  PlanView v;
+  plan_layout(const_cast<void*>(plan), M, ad->n, &v);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (sort_rows(X, w.Xs, h, v, st) != QLORA_OK || sort_rows(dY, w.Ds, o, v, st) != QLORA_OK) return QLORA_ERR_CUDA;
+  rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, st);
+  if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st);
+  if (rc != QLORA_OK) return rc;
+  PackJob ju{}, jt{};
+  ju.P = w.PU;
+  ju.slots = w.SU;
+  ju.splits = shrink_splits(M, ad->n, o);
+  jt.P = T_saved ? nullptr : w.PT;
+  jt.given = T_saved;
+  jt.slots = w.ST;
+  jt.splits = shrink_splits(M, ad->n, h);
+  rc = launch_pack(ju, &jt, ad->s, r, MD_PARTS, v, st);
+  if (rc != QLORA_OK) return rc;
+  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
+  if (rc != QLORA_OK) return rc;
+  rc = launch_multi_pair<true>(dY, w.Ds, w.SU, ad, w.Wd, o, h, MD_PARTS, dX, dx_dtype == QLORA_DTYPE_BF16, w, v, st);
+  if (rc != QLORA_OK) return rc;
+  return launch_multi_grad(X, dY, w, ad, o, h, dL1, dL2, v, st);
+}
 
 }  // extern "C"
 

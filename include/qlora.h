@@ -244,6 +244,60 @@ int qlora_linear_bwd_dropout(const qlora_nf4_t* Wq, const void* X, const void* d
                              float* dL1, float* dL2,
                              void* ws, size_t ws_bytes, void* stream);
 
+/* Many adapters beside one frozen weight: token i of a batch uses adapter
+ * a_i of a bank (the LoRA equation with factors chosen per token; no
+ * counterpart on the pages, whose layer has one adapter).
+ *
+ * qlora_adapters_t: the bank, all pointers device, read-only.
+ *   L1 : bf16 [n][h][r],  L2 : bf16 [n][r][o],  s : fp32 [n], 16- (s: 4-) byte
+ *   aligned;  1 <= n <= 65535;  8 <= r <= 256, r % 8 == 0.  Adapters of smaller
+ *   rank are padded with zero columns of L1 and rows of L2.
+ * qlora_adapter_plan: groups the tokens of a batch by adapter, once for all
+ *   layers that the batch goes through (the plan does not depend on the bank).
+ *   adapter : int32 [M], device; a value outside 0 .. n - 1 (for example -1)
+ *             means no adapter: the token gets the base product alone.
+ *   plan    : device, qlora_adapter_plan_size(M, n) bytes, written; it does not
+ *             refer to `adapter` afterwards.  M <= 2^28.  Calls only read it, so
+ *             several may use one plan at a time.
+ *   One adapter may have any number of tokens, in any order; batches in which
+ *   each adapter's tokens are contiguous are handled in place, others are
+ *   gathered into the workspace first.                                      */
+typedef struct qlora_adapters_t {
+    const void*  L1;
+    const void*  L2;
+    const float* s;
+    int32_t      n;
+    int32_t      r;
+} qlora_adapters_t;
+size_t qlora_adapter_plan_size(int64_t M, int n);
+int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, size_t plan_bytes, void* stream);
+
+/* qlora_multi_linear_fwd / qlora_multi_linear_bwd - the linear layer with a
+ * bank:
+ *   T_i = X_i L1[a_i],   Y_i = X_i W' + s[a_i] T_i L2[a_i]
+ *   U_i = dY_i L2[a_i]^T,   dX_i = dY_i W'^T + s[a_i] U_i L1[a_i]^T
+ *   dL1[a] = s[a] sum_{a_i = a} X_i^T U_i   (fp32 [n][h][r])
+ *   dL2[a] = s[a] sum_{a_i = a} T_i^T dY_i  (fp32 [n][r][o])
+ * Tokens without adapter have T = U = 0; adapters without tokens get zero
+ * gradients (dL1, dL2 are written in full).  M, X, dY, Y, dX, T_save, T_saved
+ * and the weight as in qlora_linear_fwd / qlora_linear_bwd; plan: of the same M
+ * and n, complete on `stream`; ws: device workspace of
+ * qlora_multi_linear_*_workspace_size() bytes.
+ * W' is bf16; products are bf16 x bf16 accumulated in fp32.  T and U stay in
+ * fp32 and enter the W' product as two bf16 parts (16 bits), the gradients as
+ * three (24 bits); sums are added in a fixed order, so results repeat bit for
+ * bit.  A token's outputs depend on its own row and adapter alone, and an
+ * adapter's gradients on its own tokens alone, infinities and NaN included.  */
+size_t qlora_multi_linear_fwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
+size_t qlora_multi_linear_bwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
+int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, const qlora_adapters_t* adapters,
+                           const void* plan, size_t plan_bytes, void* Y, int y_dtype, float* T_save,
+                           void* ws, size_t ws_bytes, void* stream);
+int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY, int64_t M,
+                           const qlora_adapters_t* adapters, const void* plan, size_t plan_bytes,
+                           const float* T_saved, void* dX, int dx_dtype, float* dL1, float* dL2,
+                           void* ws, size_t ws_bytes, void* stream);
+
 /* Paged optimizer for the LoRA parameters (walkthrough §4 "Paged Optimizer"
  * and "训练" step 6; neura.market "How It Works"): the optimizer state lives
  * in NVIDIA unified memory, which the driver pages between device and host
