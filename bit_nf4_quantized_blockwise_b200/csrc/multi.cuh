@@ -265,6 +265,8 @@ struct ShrinkParams {
   int K, r;
   int k_per_split;     // a multiple of 64
   float* P;            // [splits][M][r]
+  float* zero;         // also zeroed by the grid: the accumulator of the decode kernel, or null
+  int64_t zero_len;    // a multiple of 4
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -304,6 +306,11 @@ __global__ void __launch_bounds__(MS_THREADS) multi_shrink_kernel(const ShrinkPa
   constexpr int kStage = ms_stage_bytes<RP, kKN>();
   constexpr int kBPitch = ms_b_pitch<RP, kKN>();
   const int tile = blockIdx.x;
+  pdl_launch_dependents();  // a decode kernel that follows may start its weight stream now
+  if (p.zero != nullptr)
+    for (int64_t q = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * MS_THREADS + threadIdx.x;
+         q < p.zero_len / 4; q += static_cast<int64_t>(gridDim.x) * gridDim.y * MS_THREADS)
+      reinterpret_cast<float4*>(p.zero)[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (tile >= v.head->tiles) return;
   const int grp = plan_find(v.grp_tile0, v.head->groups, tile);
   const int row0 = v.grp_start[grp] + MP_TILE * (tile - v.grp_tile0[grp]);

@@ -822,7 +822,7 @@ int linear_fwd_impl(const qlora_nf4_t* Wq, const void* X, int64_t M, const void*
       cfg.numAttrs = 1;
       return cudaLaunchKernelEx(&cfg, kernel, mc, mx, dp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
     };
-    rc = M <= 8 ? launch(small_m_mma_kernel<1>) : launch(small_m_mma_kernel<2>);
+    rc = M <= 8 ? launch(small_m_mma_kernel<1, false>) : launch(small_m_mma_kernel<2, false>);
     if (rc != QLORA_OK) return rc;
     if (y_dtype == QLORA_DTYPE_BF16) {
       LaunchScope ls(QLORA_KERNEL_AUX, st);
@@ -1513,7 +1513,11 @@ int shrink_splits(int64_t M, int n, int64_t K) {
   return static_cast<int>(div_up(K / MS_K, per));
 }
 
+// Forward calls of up to this many tokens stream the 4-bit weight through the decode kernel.
+constexpr int64_t kMultiDecodeMax = 32;
+
 struct MultiWs {
+  float* Yacc;     // [M][o] fp32 accumulator of the decode forward (bf16 output)
   uint16_t* Xs;    // [M][h] rows of X in sorted order
   uint16_t* Ds;    // [M][o] rows of dY in sorted order (backward)
   float* PT;       // parts of T (backward: only when T is recomputed)
@@ -1537,8 +1541,13 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   const int64_t pairs = (sm_count() + 1) / 2;
   const int64_t slot_bytes = max_slots(M, n) * MP_SLOT_ROWS * rank_pad(r) * (bwd ? 3 : 2) * 2;
   MultiWs w{};
-  w.Xs = static_cast<uint16_t*>(take(M * h * 2));
   w.PT = static_cast<float*>(take(shrink_splits(M, n, h) * M * r * 4));
+  if (!bwd && M <= kMultiDecodeMax) {
+    w.Yacc = static_cast<float*>(take(M * o * 4));
+    w.bytes = off;
+    return w;
+  }
+  w.Xs = static_cast<uint16_t*>(take(M * h * 2));
   w.ST = static_cast<uint16_t*>(take(slot_bytes));
   if (bwd) {
     w.Ds = static_cast<uint16_t*>(take(M * o * 2));
@@ -1575,7 +1584,8 @@ int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, cudaS
 
 // Parts of A B[a] of every group: A [M][K]; kKN: B [n][K][r], else [n][r][K].
 template <bool kKN>
-int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, cudaStream_t st) {
+int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, cudaStream_t st,
+                  float* zero = nullptr, int64_t zero_len = 0) {
   const int splits = shrink_splits(v.M, v.n, K);
   ShrinkParams p{};
   p.A = static_cast<const uint16_t*>(A);
@@ -1586,6 +1596,8 @@ int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, cons
   p.r = r;
   p.k_per_split = static_cast<int>(div_up(K / MS_K, splits)) * MS_K;
   p.P = P;
+  p.zero = zero;
+  p.zero_len = zero_len;
   if (r <= 16) return launch_shrink_as<16, kKN>(p, splits, v, st);
   if (r <= 32) return launch_shrink_as<32, kKN>(p, splits, v, st);
   if (r <= 64) return launch_shrink_as<64, kKN>(p, splits, v, st);
@@ -1687,6 +1699,74 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   return launch_status();
 }
 
+// The decode forward: the split-K product T = X L1 of the groups, which also
+// zeroes the accumulator, and the weight stream as its programmatic dependent.
+int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapters_t* ad, void* Y, int y_dtype,
+                        float* T_save, const MultiWs& w, const PlanView& v, cudaStream_t st) {
+  const int64_t M = v.M, o = Wq->o, h = Wq->h;
+  const int r = ad->r;
+  float* acc = y_dtype == QLORA_DTYPE_F32 ? static_cast<float*>(Y) : w.Yacc;
+  const int rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st, acc, M * o);
+  if (rc != QLORA_OK) return rc;
+  CUtensorMap mc, mx;
+  if (!map_u8(&mc, Wq->codes, h / 2, o, h / 2, SD_UNIT_K / 2, SK_BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map_bf16_3d(&mx, X, 64, h / 64, M, 128, h * 2, 64, SD_UNIT_BLOCKS, static_cast<uint32_t>(M)))
+    return QLORA_ERR_CUDA;
+  DecodeParams dp{};
+  dp.M = static_cast<int>(M);
+  dp.N = static_cast<int>(o);
+  dp.k_units = static_cast<int>(div_up(h, SD_UNIT_K));
+  dp.blocks_per_row = static_cast<int>(h / 64);
+  dp.r = r;
+  dp.units = div_up(o, SK_BN) * dp.k_units;
+  dp.slot_bytes = static_cast<int>(div_up(SD_CODE_BYTES + M * SD_UNIT_BLOCKS * SD_X_ROW_BYTES, 1024) * 1024);
+  const int64_t scratch = SD_LORA_THREADS * SD_LORA_MT * SD_LORA_COLS * 4;
+  dp.low_bytes = static_cast<int>(div_up(SD_BAR_BYTES + M * r * 4 + scratch, 1024) * 1024);
+  dp.P = w.PT;
+  dp.n_part = shrink_splits(M, ad->n, h);
+  dp.T_out = T_save;
+  dp.L2 = static_cast<const uint16_t*>(ad->L2);
+  dp.absmax_fp8 = Wq->absmax_fp8;
+  dp.dq_scale = Wq->dq_scale;
+  dp.dq_mean = Wq->dq_mean;
+  dp.absmax32 = Wq->absmax;
+  dp.out = acc;
+  std::memcpy(dp.codebook, Wq->codebook, sizeof(dp.codebook));
+  dp.scales = ad->s;
+  dp.groups = &v.head->groups;
+  dp.grp_adapter = v.grp_adapter;
+  dp.grp_start = v.grp_start;
+  dp.grp_end = v.grp_end;
+  dp.perm = v.perm;
+  dp.owner = v.owner;
+  const int64_t grid = dp.units < sm_count() ? dp.units : sm_count();
+  auto launch = [&](auto kernel, int threads) {
+    if (set_smem(kernel, SD_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+    LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = SD_SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mc, mx, dp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  };
+  const int lc = M <= 8    ? launch(small_m_mma_kernel<1, true>, sd_threads(1))
+                 : M <= 16 ? launch(small_m_mma_kernel<2, true>, sd_threads(2))
+                           : launch(small_m_mma_kernel<4, true>, sd_threads(4));
+  if (lc != QLORA_OK) return lc;
+  if (y_dtype == QLORA_DTYPE_BF16) {
+    LaunchScope ls(QLORA_KERNEL_AUX, st);
+    f32_to_bf16_kernel<<<static_cast<unsigned>(grid_for(M * o, 256, sm_count() * 4)), 256, 0, st>>>(
+        acc, M * o, static_cast<uint16_t*>(Y));
+  }
+  return launch_status();
+}
+
 int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlora_adapters_t* ad, int64_t o,
                       int64_t h, float* dL1, float* dL2, const PlanView& v, cudaStream_t st) {
   const int64_t M = v.M, rp = rank_pad(ad->r), width = MD_PARTS * rp, rows = max_slots(M, v.n) * MP_SLOT_ROWS;
@@ -1777,6 +1857,7 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   PlanView v;
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
   if (sort_rows(X, w.Xs, h, v, st) != QLORA_OK) return QLORA_ERR_CUDA;
   rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st);
   if (rc != QLORA_OK) return rc;
