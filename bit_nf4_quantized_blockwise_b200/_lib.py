@@ -8,6 +8,7 @@ the library is missing or a call fails, they raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
@@ -244,6 +245,28 @@ def _check_linear(Wq: "NF4Weight", X, L1, L2, Y=None, T=None, dY=None, dX=None, 
     return M, r
 
 
+def _fits(t: torch.Tensor, shape, *dtypes) -> bool:
+    """What _need asks, as one cheap test: a decode call lasts a few microseconds on the device, so the
+    many-adapter calls check with this and let _need name what is wrong."""
+    return t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+
+
+@functools.lru_cache(maxsize=64)
+def _codebook_of(codebook: Tuple[float, ...]):
+    return _codebook_array(codebook)
+
+
+def _call(fn, what: str, dev: torch.device, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != QLORA_OK:
+        raise QLoRAError(what, status)
+
+
 def _codebook_array(codebook: Sequence[float]):
     vals = [float(v) for v in (codebook.tolist() if hasattr(codebook, "tolist") else codebook)]
     if len(vals) != 16:
@@ -278,7 +301,7 @@ class NF4Weight:
         s.dq_mean = self.dq_mean.data_ptr() if self.dq_mean is not None else None
         s.o = self.o
         s.h = self.h
-        s.codebook = _codebook_array(self.codebook)
+        s.codebook = _codebook_of(self.codebook) if type(self.codebook) is tuple else _codebook_array(self.codebook)
         s.block = 64
         s.dq_block = 256
         s.absmax = self.absmax.data_ptr() if self.absmax is not None else None
@@ -464,11 +487,12 @@ def qlora_merge_bf16(Wq: NF4Weight, L1: torch.Tensor, L2: torch.Tensor, s: float
     return out
 
 
-@dataclass
+@dataclass(frozen=True)
 class AdapterBank:
     """Adapters that share one frozen weight: bf16 L1 [n][h][r] and L2 [n][r][o]
     (adapters of smaller rank padded with zeros), fp32 scales s [n] on the
-    device.  Views of one adapter (bank.L1[a]) are its factors."""
+    device.  Views of one adapter (bank.L1[a]) are its factors, which may be
+    written in place."""
     L1: torch.Tensor
     L2: torch.Tensor
     s: torch.Tensor
@@ -481,20 +505,21 @@ class AdapterBank:
         _need(self.L2, "L2", (n, r, self.L2.shape[2]), (torch.bfloat16,))
         _need(self.s, "s", (n,), (torch.float32,))
         _same_device(self.L1, self.L2, self.s)
+        object.__setattr__(self, "dims", (n, h, r, self.L2.shape[2]))
 
     @property
     def n(self) -> int:
-        return self.L1.shape[0]
+        return self.dims[0]
 
     @property
     def r(self) -> int:
-        return self.L1.shape[2]
+        return self.dims[2]
 
     def struct(self) -> qlora_adapters_t:
-        return qlora_adapters_t(self.L1.data_ptr(), self.L2.data_ptr(), self.s.data_ptr(), self.n, self.r)
+        return qlora_adapters_t(self.L1.data_ptr(), self.L2.data_ptr(), self.s.data_ptr(), self.dims[0], self.dims[2])
 
 
-@dataclass
+@dataclass(frozen=True)
 class AdapterPlan:
     """The tokens of a batch grouped by adapter (qlora_adapter_plan)."""
     buffer: torch.Tensor
@@ -522,35 +547,58 @@ def qlora_adapter_plan(adapter: torch.Tensor, n: int, plan: Optional[AdapterPlan
     dev = _require_cuda(adapter)
     if plan is None:
         plan = AdapterPlan(torch.empty(size, dtype=torch.uint8, device=dev), M, int(n))
-    with torch.cuda.device(dev):
-        _check(L.qlora_adapter_plan(_p(adapter), M, plan.n, _p(plan.buffer), plan.buffer.numel(), _stream(dev)),
-               "qlora_adapter_plan")
+    _call(L.qlora_adapter_plan, "qlora_adapter_plan", dev, adapter.data_ptr(), M, plan.n, plan.buffer.data_ptr(),
+          plan.buffer.numel())
     return plan
 
 
-def _check_multi(Wq: NF4Weight, X, bank: AdapterBank, plan: AdapterPlan, Y=None, T=None, dY=None, dX=None, dL1=None,
-                 dL2=None):
-    """Every operand of the many-adapter layer against the weight, the bank and the plan."""
-    _check_weight(Wq)
+_OUT = (torch.float32, torch.bfloat16)
+
+
+def _check_multi(Wq: NF4Weight, bank: AdapterBank, plan: AdapterPlan, X, *rest):
+    """Every operand of the many-adapter layer against the weight, the bank and
+    the plan; rest: (tensor or None, name, shape by its letters, dtypes)."""
     o, h = Wq.o, Wq.h
+    w = Wq.codes
+    if w is None or w.numel() != o * h // 2 or w.dtype is not torch.uint8 or not w.is_contiguous():
+        _check_weight(Wq)
+    consts = (Wq.absmax,) if Wq.absmax is not None else (Wq.absmax_fp8, Wq.dq_scale, Wq.dq_mean)
+    if Wq.absmax is not None or any(c is None for c in consts) or consts[0].numel() != o * h // 64 or \
+            consts[0].dtype is not torch.uint8 or consts[1].numel() != o * h // 16384 or \
+            consts[1].dtype is not torch.float32 or consts[2].numel() != 1 or consts[2].dtype is not torch.float32 or \
+            not (consts[0].is_contiguous() and consts[1].is_contiguous()):
+        _check_weight(Wq)
     if X.dim() != 2 or X.shape[1] != h:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected (M, {h})")
     M = X.shape[0]
-    n, hb, r = bank.L1.shape
-    if hb != h or bank.L2.shape[2] != o:
-        raise ValueError(f"the bank is for {hb} x {bank.L2.shape[2]}, the weight is {h} x {o}")
+    n, hb, r, ob = bank.dims
+    if hb != h or ob != o:
+        raise ValueError(f"the bank is for {hb} x {ob}, the weight is {h} x {o}")
     if plan.M != M or plan.n != n:
         raise ValueError(f"plan is for {plan.M} tokens and {plan.n} adapters, not {M} and {n}")
-    _need(X, "X", (M, h), (torch.bfloat16,))
-    _need(Y, "Y", (M, o), (torch.float32, torch.bfloat16))
-    _need(T, "T", (M, r), (torch.float32,))
-    _need(dY, "dY", (M, o), (torch.bfloat16,))
-    _need(dX, "dX", (M, h), (torch.float32, torch.bfloat16))
-    _need(dL1, "dL1", (n, h, r), (torch.float32,))
-    _need(dL2, "dL2", (n, r, o), (torch.float32,))
-    _same_device(Wq.codes, Wq.absmax_fp8, Wq.dq_scale, Wq.dq_mean, Wq.absmax, X, bank.L1, plan.buffer, Y, T, dY, dX,
-                 dL1, dL2)
+    if not _fits(X, (M, h), torch.bfloat16):
+        _need(X, "X", (M, h), (torch.bfloat16,))
+    size = {"M": M, "h": h, "o": o, "n": n, "r": r}
+    devs = {X.get_device(), w.get_device(), bank.L1.get_device(), plan.buffer.get_device()}
+    devs.update([c.get_device() for c in consts])
+    for t, name, letters, dtypes in rest:
+        if t is not None:
+            shape = tuple([size[c] for c in letters])
+            if not _fits(t, shape, *dtypes):
+                _need(t, name, shape, dtypes)
+            devs.add(t.get_device())
+    if len(devs) > 1:
+        raise ValueError(f"operands are on different devices: {sorted(devs)}")
+    if not X.is_cuda:
+        raise ValueError("libqlora takes CUDA tensors (device memory)")
     return M, n, r
+
+
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+
+
+def _or_null(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, plan: AdapterPlan,
@@ -560,8 +608,8 @@ def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, pl
     """Y_i = X_i W' + s[a_i] X_i L1[a_i] L2[a_i], each token with its own adapter
     of the bank (or none).  Returns (Y, T), T_i = X_i L1[a_i] in fp32 (None
     unless save_T)."""
-    M, n, r = _check_multi(Wq, X, bank, plan, Y=Y, T=T_save)
-    dev = _require_cuda(X, Wq.codes, bank.L1)
+    M, n, r = _check_multi(Wq, bank, plan, X, (Y, "Y", "Mo", _OUT), (T_save, "T", "Mr", _F32))
+    dev = X.device
     if Y is None:
         Y = torch.empty(M, Wq.o, dtype=y_dtype, device=dev)
     if T_save is None and save_T:
@@ -570,11 +618,9 @@ def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, pl
     wsb = L.qlora_multi_linear_fwd_workspace_size(Wq.o, Wq.h, M, n, r)
     if ws is None or ws.numel() * ws.element_size() < wsb:
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(L.qlora_multi_linear_fwd(ctypes.byref(Wq.struct()), _p(X), M, ctypes.byref(bank.struct()),
-                                        _p(plan.buffer), plan.buffer.numel(), _p(Y), _dtype_code(Y.dtype), _p(T_save),
-                                        _p(ws), ws.numel() * ws.element_size(), _stream(dev)),
-               "qlora_multi_linear_fwd")
+    _call(L.qlora_multi_linear_fwd, "qlora_multi_linear_fwd", dev, Wq.struct(), X.data_ptr(), M, bank.struct(),
+          plan.buffer.data_ptr(), plan.buffer.numel(), Y.data_ptr(), _dtype_code(Y.dtype), _or_null(T_save),
+          ws.data_ptr(), ws.numel() * ws.element_size())
     return Y, T_save
 
 
@@ -584,8 +630,9 @@ def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, ban
                            dL2: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """Returns (dX, dL1 [n][h][r], dL2 [n][r][o]) of <Y, dY>; adapters without
     tokens get zero gradients, W is frozen."""
-    M, n, r = _check_multi(Wq, X, bank, plan, T=T_saved, dY=dY, dX=dX, dL1=dL1, dL2=dL2)
-    dev = _require_cuda(X, Wq.codes, bank.L1)
+    M, n, r = _check_multi(Wq, bank, plan, X, (dY, "dY", "Mo", _BF16), (T_saved, "T", "Mr", _F32),
+                           (dX, "dX", "Mh", _OUT), (dL1, "dL1", "nhr", _F32), (dL2, "dL2", "nro", _F32))
+    dev = X.device
     if dX is None:
         dX = torch.empty(M, Wq.h, dtype=dx_dtype, device=dev)
     if dL1 is None:
@@ -596,12 +643,9 @@ def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, ban
     wsb = L.qlora_multi_linear_bwd_workspace_size(Wq.o, Wq.h, M, n, r)
     if ws is None or ws.numel() * ws.element_size() < wsb:
         ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(L.qlora_multi_linear_bwd(ctypes.byref(Wq.struct()), _p(X), _p(dY), M, ctypes.byref(bank.struct()),
-                                        _p(plan.buffer), plan.buffer.numel(), _p(T_saved), _p(dX),
-                                        _dtype_code(dX.dtype), _p(dL1), _p(dL2), _p(ws),
-                                        ws.numel() * ws.element_size(), _stream(dev)),
-               "qlora_multi_linear_bwd")
+    _call(L.qlora_multi_linear_bwd, "qlora_multi_linear_bwd", dev, Wq.struct(), X.data_ptr(), dY.data_ptr(), M,
+          bank.struct(), plan.buffer.data_ptr(), plan.buffer.numel(), _or_null(T_saved), dX.data_ptr(),
+          _dtype_code(dX.dtype), dL1.data_ptr(), dL2.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dX, dL1, dL2
 
 

@@ -1292,10 +1292,6 @@ constexpr int SD_LORA_WARP0 = 1 + 4 * SD_GROUPS;        // warps 17 .. 19: the L
 constexpr int SD_THREADS = 640;
 constexpr int SD_LORA_THREADS = SD_THREADS - 32 * SD_LORA_WARP0;
 constexpr int SD_MAX_TOKENS = 16;
-// 17 .. 32 tokens keep 64 accumulator and token registers a thread: three groups, so that a
-// thread may have 128.
-constexpr int sd_groups(int ng) { return ng <= 2 ? SD_GROUPS : 3; }
-constexpr int sd_threads(int ng) { return SD_THREADS - 128 * (SD_GROUPS - sd_groups(ng)); }
 static_assert(SD_LORA_THREADS >= 32, "at least one LoRA warp");
 static_assert(SD_MAX_STAGES % SD_PRODUCERS == 0, "each producer lane owns fixed slots");
 
@@ -1319,129 +1315,7 @@ struct DecodeParams {
   const float* absmax32;  // single-level constants (no double quantization), or null
   float* out;          // fp32 [M][N], zeroed beforehand, accumulated
   float codebook[16];
-  // many adapters (L2 is a bank [n][r][o]; P and T are in the groups' order)
-  const float* scales;       // [n]
-  const int* groups;         // number of groups (device)
-  const int* grp_adapter;    // [groups]
-  const int* grp_start;      // [groups] first token of the group in the groups' order
-  const int* grp_end;        // [groups]
-  const int* perm;           // [M] token at each place of the groups' order
-  const int* owner;          // [M] adapter of a token, -1: none
 };
-
-// The LoRA term of a decode batch whose tokens use different adapters, by
-// SD_LORA_THREADS threads: T from its parts, then Y[m][n] += s[a] sum_j T[m][j]
-// L2[a][j][n] for an even share of the columns.  The share is a few 16-byte
-// column vectors wide (7 of 8192 columns, 19 of 22016), so the threads stand
-// as (row slice, vector): each reads every slices-th row of L2 at its vector,
-// eight rows in flight, for up to two tokens of the group, and the slices'
-// sums are added through shared memory in order.  L2 of every adapter is read
-// once per CTA column share, behind the weight stream of the other warps.
-constexpr int SD_LORA_COLS = 8;
-constexpr int SD_LORA_MT = 2;
-template <int kThreads>
-__device__ __forceinline__ void decode_lora_groups(const DecodeParams& p, float* Ts, float* red, int tid) {
-  const int groups = *p.groups;
-  const int64_t G = gridDim.x;
-  const int nt4 = p.r / 4;
-  const int64_t part4 = static_cast<int64_t>(p.M) * nt4;
-  const float4* P4 = reinterpret_cast<const float4*>(p.P);
-  for (int g = 0; g < groups; ++g) {
-    const int q0 = p.grp_start[g] * nt4, q1 = p.grp_end[g] * nt4;
-    for (int q = q0 + tid; q < q1; q += kThreads) {
-      float4 a[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) a[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      int b = 0;
-      for (; b + 8 <= p.n_part; b += 8) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float4 v = __ldg(P4 + (b + u) * part4 + q);
-          a[u].x += v.x, a[u].y += v.y, a[u].z += v.z, a[u].w += v.w;
-        }
-      }
-      for (; b < p.n_part; ++b) {
-        const float4 v = __ldg(P4 + b * part4 + q);
-        a[0].x += v.x, a[0].y += v.y, a[0].z += v.z, a[0].w += v.w;
-      }
-#pragma unroll
-      for (int u = 4; u > 0; u >>= 1)
-#pragma unroll
-        for (int i = 0; i < u; ++i)
-          a[i].x += a[i + u].x, a[i].y += a[i + u].y, a[i].z += a[i + u].z, a[i].w += a[i + u].w;
-      reinterpret_cast<float4*>(Ts)[q] = a[0];
-      if (blockIdx.x == 0 && p.T_out != nullptr)
-        reinterpret_cast<float4*>(p.T_out)[static_cast<int64_t>(p.perm[q / nt4]) * nt4 + q % nt4] = a[0];
-    }
-  }
-  if (blockIdx.x == 0 && p.T_out != nullptr)
-    for (int q = tid; q < p.M * nt4; q += kThreads)
-      if (p.owner[q / nt4] < 0) reinterpret_cast<float4*>(p.T_out)[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-  const int64_t cols = p.N / SD_LORA_COLS;
-  const int64_t c1 = cols * (blockIdx.x + 1) / G;
-  for (int64_t c0 = cols * blockIdx.x / G; c0 < c1; c0 += kThreads) {
-    const int nv = static_cast<int>(c1 - c0 < kThreads ? c1 - c0 : kThreads);  // vectors of this pass
-    const int slices = kThreads / nv;
-    const int slice = tid / nv, vec = tid - slice * nv;
-    const bool active = slice < slices;
-    for (int g = 0; g < groups; ++g) {
-      const int a = p.grp_adapter[g];
-      const float s = p.scales[a];
-      const uint16_t* L2 = p.L2 + static_cast<int64_t>(a) * p.r * p.N + (c0 + vec) * SD_LORA_COLS;
-      for (int m0 = p.grp_start[g]; m0 < p.grp_end[g]; m0 += SD_LORA_MT) {
-        const int mt = min(SD_LORA_MT, p.grp_end[g] - m0);
-        if (active) {
-          float acc[SD_LORA_MT][SD_LORA_COLS];
-#pragma unroll
-          for (int m = 0; m < SD_LORA_MT; ++m)
-#pragma unroll
-            for (int c = 0; c < SD_LORA_COLS; ++c) acc[m][c] = 0.0f;
-          for (int j0 = slice; j0 < p.r; j0 += 8 * slices) {
-            uint4 w[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int j = j0 + u * slices;
-              w[u] = j < p.r ? __ldg(reinterpret_cast<const uint4*>(L2 + static_cast<int64_t>(j) * p.N))
-                             : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int j = j0 + u * slices;
-              if (j >= p.r) break;
-              const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-              for (int m = 0; m < SD_LORA_MT; ++m) {
-                if (m >= mt) break;
-                const float t = Ts[(m0 + m) * p.r + j];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  acc[m][2 * c] = fmaf(t, __uint_as_float(ws[c] << 16), acc[m][2 * c]);
-                  acc[m][2 * c + 1] = fmaf(t, __uint_as_float(ws[c] & 0xFFFF0000u), acc[m][2 * c + 1]);
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int m = 0; m < SD_LORA_MT; ++m) {
-            if (m >= mt) break;
-            float4* d = reinterpret_cast<float4*>(red) + ((slice * SD_LORA_MT + m) * nv + vec) * 2;
-            d[0] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
-            d[1] = make_float4(acc[m][4], acc[m][5], acc[m][6], acc[m][7]);
-          }
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-        for (int q = tid; q < mt * nv * SD_LORA_COLS; q += kThreads) {
-          const int m = q / (nv * SD_LORA_COLS), c = q - m * nv * SD_LORA_COLS;
-          float sum = 0.0f;
-          for (int k = 0; k < slices; ++k) sum += red[(k * SD_LORA_MT + m) * nv * SD_LORA_COLS + c];
-          atomicAdd(p.out + static_cast<int64_t>(p.perm[m0 + m]) * p.N + c0 * SD_LORA_COLS + c, s * sum);
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-      }
-    }
-  }
-}
 
 // D (16 x 8, fp32) += A (16 x 16, bf16, row) * B (16 x 8, bf16, col).
 __device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -1512,15 +1386,14 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
-// NG token groups of 8 (NG = 1: M <= 8, NG = 2: M <= 16, NG = 4: M <= 32).
-// kMulti: the tokens use different adapters (decode_lora_groups); its scratch
-// lies behind T below the ring.
-template <int NG, bool kMulti>
-__global__ void __launch_bounds__(sd_threads(NG), 1)
+// NG token groups of 8 (NG = 1: M <= 8, NG = 2: M <= 16).  kLora = false
+// (tokens with different adapters) only sums T for the kernel that adds the
+// adapters' term.
+template <int NG, bool kLora>
+__global__ void __launch_bounds__(SD_THREADS, 1)
     small_m_mma_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  constexpr int kGroups = sd_groups(NG), kLoraWarp0 = 1 + 4 * kGroups;
   const uint32_t r0 = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   const uint32_t lo0 = r0 + static_cast<uint32_t>(p.low_bytes);
   const uint32_t toff = pair_tab_offset(smem_raw, lo0);
@@ -1596,7 +1469,7 @@ __global__ void __launch_bounds__(sd_threads(NG), 1)
       if (first < lane) first = lane;
       for (int n = first; n <= issued; n += SD_PRODUCERS) mbar_wait(&full[n % S], (n / S) & 1, 3);
     }
-  } else if (warp < kLoraWarp0) {
+  } else if (warp < SD_LORA_WARP0) {
     // ---------------- MMA warps: warp wq of group grp owns rows 32 wq .. 32 wq + 31
     // of its units; fragment rows g and g + 8 of each 16-row half rt
     const int grp = (warp - 1) >> 2;
@@ -1656,7 +1529,7 @@ __global__ void __launch_bounds__(sd_threads(NG), 1)
           u.w[3] = static_cast<uint32_t>(256 - static_cast<int>(b0 & 255));
         }
       }
-      pf.step(kGroups);
+      pf.step(SD_GROUPS);
     };
 #pragma unroll
     for (int i = 0; i < kPre; ++i) fetch(uc[i]);
@@ -1785,23 +1658,19 @@ __global__ void __launch_bounds__(sd_threads(NG), 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[cs]);
-        cur.step(kGroups);
+        cur.step(SD_GROUPS);
       }
     }
     flush();
-  } else {
+  } else if constexpr (kLora) {
     // ---------------- LoRA term: T = X L1 from its per-CTA partials (the same
     // fixed order in every CTA), then Y[m][n] += s sum_j T[m][j] L2[j][n] for
     // an even share of the output rows.  The partials are read four columns at
     // a time with eight partials in flight per thread, so the sum costs a few
     // memory latencies whatever M.
-    const int tid = threadIdx.x - 32 * kLoraWarp0;
+    const int tid = threadIdx.x - 32 * SD_LORA_WARP0;
     pdl_wait();  // the partials of T and the zeroed output come from the rank-r kernel
     float* Ts = reinterpret_cast<float*>(smem_raw + r0 + SD_BAR_BYTES);
-    if constexpr (kMulti) {
-      decode_lora_groups<SD_LORA_THREADS>(p, Ts, Ts + p.M * p.r, tid);
-      return;
-    }
     const int nt = p.M * p.r;  // a multiple of 8
     const float4* P4 = reinterpret_cast<const float4*>(p.P);
     for (int q = tid; q < nt / 4; q += SD_LORA_THREADS) {
@@ -1845,6 +1714,22 @@ __global__ void __launch_bounds__(sd_threads(NG), 1)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         if (m < p.M) atomicAdd(p.out + static_cast<int64_t>(m) * p.N + n, p.s * sum[m]);
+    }
+  } else {
+    // ---------------- tokens with different adapters: T from its parts, once, in a
+    // fixed order, for the kernel that adds the adapters' term
+    pdl_wait();
+    const int nt4 = p.M * p.r / 4;
+    const float4* P4 = reinterpret_cast<const float4*>(p.P);
+    for (int q = static_cast<int>(blockIdx.x) * SD_LORA_THREADS + threadIdx.x - 32 * SD_LORA_WARP0; q < nt4;
+         q += static_cast<int>(gridDim.x) * SD_LORA_THREADS) {
+      float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int b = 0; b < p.n_part; ++b) {
+        const float4 x = __ldg(P4 + static_cast<int64_t>(b) * nt4 + q);
+        f.x += x.x, f.y += x.y, f.z += x.z, f.w += x.w;
+      }
+      reinterpret_cast<float4*>(p.T_out)[q] = f;
     }
   }
 }

@@ -25,6 +25,8 @@
 // and adapter alone, in fp32; a finite batch never gets there.
 #pragma once
 
+#include "qlora.h"
+
 #include "common.cuh"
 #include "gemm.cuh"
 #include "pairgemm.cuh"
@@ -474,6 +476,150 @@ __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, con
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = isfinite(f[j]) ? x[j] - f[j] : 0.0f;
     }
+  }
+}
+
+// ====================================================================== adapters of a decode batch
+
+// The adapter term of a batch of up to 32 tokens, added to the finished base
+// product: Y[i] = acc[i] + s[a] sum_j T[i][j] L2[a][j] for one group
+// (blockIdx.y) and 128 columns (blockIdx.x); blockIdx.y = max_groups: the tokens
+// without adapter.  L2 is the only large operand (2 r o bytes an adapter), read
+// once for up to four tokens: 16 threads of 8 columns each by 16 slices of the
+// ranks, four rows a thread in flight.  The first rows are loaded before the
+// wait for the base product.  T is summed from its parts in order, the slices
+// through shared memory in order.  A pass of its own and not a share of the
+// decode kernel's warps: three warps an SM cannot keep enough loads in flight
+// beside a ring that fills the shared memory (16 adapters of rank 64, 8192 x
+// 22016: 114 to 140 us for the two in one kernel, 68 + EXPAND16 apart).
+constexpr int MX_THREADS = 256;
+constexpr int MX_COLS = 128;
+constexpr int MX_SLICES = 16;
+constexpr int MX_MT = 4;
+
+struct ExpandParams {
+  const float* P;      // [parts][M][r] of T, sorted rows
+  const uint16_t* L2;  // bank [n][r][N]
+  const float* s;      // [n]
+  const float* acc;    // [M][N] base product
+  void* Y;             // [M][N], fp32 (may be acc) or bf16
+  float* T;            // [M][r], batch order, or null
+  int parts, r, N, max_groups;
+};
+
+template <bool kBf16>
+__global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const ExpandParams p, const PlanView v) {
+  __shared__ __align__(16) float Ts[MX_MT * QLORA_MAX_RANK];
+  __shared__ __align__(16) float red[MX_SLICES * MX_MT * MX_COLS];
+  const int tid = threadIdx.x;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * MX_COLS;
+  const int cols = static_cast<int>(p.N - n0 < MX_COLS ? p.N - n0 : MX_COLS);  // a multiple of 64
+  auto put = [&](int64_t m, int64_t n, float y) {
+    if constexpr (kBf16)
+      static_cast<uint16_t*>(p.Y)[m * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+    else
+      static_cast<float*>(p.Y)[m * p.N + n] = y;
+  };
+  if (static_cast<int>(blockIdx.y) == p.max_groups) {
+    pdl_wait();
+    for (int m = 0; m < v.M; ++m) {
+      if (v.owner[m] >= 0) continue;
+      if (p.T && blockIdx.x == 0)
+        for (int j = tid; j < p.r; j += MX_THREADS) p.T[static_cast<int64_t>(m) * p.r + j] = 0.0f;
+      if (kBf16)
+        for (int c = tid; c < cols; c += MX_THREADS) put(m, n0 + c, p.acc[static_cast<int64_t>(m) * p.N + n0 + c]);
+    }
+    return;
+  }
+  if (static_cast<int>(blockIdx.y) >= v.head->groups) return;
+  const int grp = blockIdx.y;
+  const int a = v.grp_adapter[grp], g0 = v.grp_start[grp], g1 = v.grp_end[grp];
+  const float s = p.s[a];
+  const int vec = tid & 15, slice = tid >> 4;
+  const bool in = 8 * vec < cols;
+  const uint16_t* L2 = p.L2 + static_cast<int64_t>(a) * p.r * p.N + n0 + 8 * vec;
+  auto load = [&](int j0, uint4 (&w)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + slice + u * MX_SLICES;
+      w[u] = in && j < p.r ? __ldg(reinterpret_cast<const uint4*>(L2 + static_cast<int64_t>(j) * p.N))
+                           : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  uint4 w[4];
+  load(0, w);
+  pdl_wait();
+  for (int m0 = g0; m0 < g1; m0 += MX_MT) {
+    const int mt = min(MX_MT, g1 - m0);
+    // T of these tokens: groups of threads take every sub-th part, then the groups are added in order
+    const int nt4 = mt * p.r / 4;  // float4s, 2 .. 256
+    const int subs = MX_THREADS / nt4;
+    const int q = tid % nt4, sub = tid / nt4;
+    if (sub < subs) {
+      const float4* src = reinterpret_cast<const float4*>(p.P + static_cast<int64_t>(m0) * p.r) + q;
+      const int64_t part4 = static_cast<int64_t>(v.M) * p.r / 4;
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = sub; k < p.parts; k += subs) {
+        const float4 x = __ldcg(src + k * part4);
+        f.x += x.x, f.y += x.y, f.z += x.z, f.w += x.w;
+      }
+      reinterpret_cast<float4*>(red)[sub * nt4 + q] = f;
+    }
+    __syncthreads();
+    if (tid < nt4) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < subs; ++k) {
+        const float4 x = reinterpret_cast<const float4*>(red)[k * nt4 + tid];
+        f.x += x.x, f.y += x.y, f.z += x.z, f.w += x.w;
+      }
+      reinterpret_cast<float4*>(Ts)[tid] = f;
+      if (p.T && blockIdx.x == 0)
+        reinterpret_cast<float4*>(p.T + static_cast<int64_t>(v.perm[m0 + 4 * tid / p.r]) * p.r)[tid % (p.r / 4)] = f;
+    }
+    __syncthreads();
+    float acc[MX_MT][8];
+#pragma unroll
+    for (int m = 0; m < MX_MT; ++m)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[m][c] = 0.0f;
+    for (int j0 = 0; j0 < p.r; j0 += 4 * MX_SLICES) {
+      if (j0 > 0 || m0 > g0) load(j0, w);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + slice + u * MX_SLICES;
+        if (j >= p.r) break;
+        const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+        for (int m = 0; m < MX_MT; ++m) {
+          if (m >= mt) break;
+          const float t = Ts[m * p.r + j];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[m][2 * c] = fmaf(t, __uint_as_float(ws[c] << 16), acc[m][2 * c]);
+            acc[m][2 * c + 1] = fmaf(t, __uint_as_float(ws[c] & 0xFFFF0000u), acc[m][2 * c + 1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MX_MT; ++m) {
+      if (m >= mt) break;
+      float4* d = reinterpret_cast<float4*>(red + (slice * MX_MT + m) * MX_COLS + 8 * vec);
+      d[0] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+      d[1] = make_float4(acc[m][4], acc[m][5], acc[m][6], acc[m][7]);
+    }
+    __syncthreads();
+    for (int q2 = tid; q2 < mt * MX_COLS; q2 += MX_THREADS) {
+      const int m = q2 / MX_COLS, c = q2 % MX_COLS;
+      if (c >= cols) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < MX_SLICES; ++k) sum += red[(k * MX_MT + m) * MX_COLS + c];
+      const int64_t row = v.perm[m0 + m];
+      put(row, n0 + c, fmaf(s, sum, p.acc[row * p.N + n0 + c]));
+    }
+    __syncthreads();
   }
 }
 

@@ -822,7 +822,7 @@ int linear_fwd_impl(const qlora_nf4_t* Wq, const void* X, int64_t M, const void*
       cfg.numAttrs = 1;
       return cudaLaunchKernelEx(&cfg, kernel, mc, mx, dp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
     };
-    rc = M <= 8 ? launch(small_m_mma_kernel<1, false>) : launch(small_m_mma_kernel<2, false>);
+    rc = M <= 8 ? launch(small_m_mma_kernel<1, true>) : launch(small_m_mma_kernel<2, true>);
     if (rc != QLORA_OK) return rc;
     if (y_dtype == QLORA_DTYPE_BF16) {
       LaunchScope ls(QLORA_KERNEL_AUX, st);
@@ -1518,6 +1518,7 @@ constexpr int64_t kMultiDecodeMax = 32;
 
 struct MultiWs {
   float* Yacc;     // [M][o] fp32 accumulator of the decode forward (bf16 output)
+  float* Tsum;     // [M][r] T of the decode forward, sorted rows
   uint16_t* Xs;    // [M][h] rows of X in sorted order
   uint16_t* Ds;    // [M][o] rows of dY in sorted order (backward)
   float* PT;       // parts of T (backward: only when T is recomputed)
@@ -1544,6 +1545,7 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   w.PT = static_cast<float*>(take(shrink_splits(M, n, h) * M * r * 4));
   if (!bwd && M <= kMultiDecodeMax) {
     w.Yacc = static_cast<float*>(take(M * o * 4));
+    w.Tsum = static_cast<float*>(take(M * r * 4));
     w.bytes = off;
     return w;
   }
@@ -1699,72 +1701,101 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   return launch_status();
 }
 
-// The decode forward: the split-K product T = X L1 of the groups, which also
-// zeroes the accumulator, and the weight stream as its programmatic dependent.
+// A kernel as the programmatic dependent of the one before it on the stream.
+template <typename K, typename... Args>
+int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// The decode forward, three launches: the split-K product T = X L1 of the
+// groups, which also zeroes the accumulator; the weight stream of the decode
+// kernels; the adapters' term and the output type.
 int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapters_t* ad, void* Y, int y_dtype,
                         float* T_save, const MultiWs& w, const PlanView& v, cudaStream_t st) {
   const int64_t M = v.M, o = Wq->o, h = Wq->h;
   const int r = ad->r;
   float* acc = y_dtype == QLORA_DTYPE_F32 ? static_cast<float*>(Y) : w.Yacc;
-  const int rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st, acc, M * o);
+  int rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st, acc, M * o);
   if (rc != QLORA_OK) return rc;
   CUtensorMap mc, mx;
-  if (!map_u8(&mc, Wq->codes, h / 2, o, h / 2, SD_UNIT_K / 2, SK_BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map_bf16_3d(&mx, X, 64, h / 64, M, 128, h * 2, 64, SD_UNIT_BLOCKS, static_cast<uint32_t>(M)))
-    return QLORA_ERR_CUDA;
-  DecodeParams dp{};
-  dp.M = static_cast<int>(M);
-  dp.N = static_cast<int>(o);
-  dp.k_units = static_cast<int>(div_up(h, SD_UNIT_K));
-  dp.blocks_per_row = static_cast<int>(h / 64);
-  dp.r = r;
-  dp.units = div_up(o, SK_BN) * dp.k_units;
-  dp.slot_bytes = static_cast<int>(div_up(SD_CODE_BYTES + M * SD_UNIT_BLOCKS * SD_X_ROW_BYTES, 1024) * 1024);
-  const int64_t scratch = SD_LORA_THREADS * SD_LORA_MT * SD_LORA_COLS * 4;
-  dp.low_bytes = static_cast<int>(div_up(SD_BAR_BYTES + M * r * 4 + scratch, 1024) * 1024);
-  dp.P = w.PT;
-  dp.n_part = shrink_splits(M, ad->n, h);
-  dp.T_out = T_save;
-  dp.L2 = static_cast<const uint16_t*>(ad->L2);
-  dp.absmax_fp8 = Wq->absmax_fp8;
-  dp.dq_scale = Wq->dq_scale;
-  dp.dq_mean = Wq->dq_mean;
-  dp.absmax32 = Wq->absmax;
-  dp.out = acc;
-  std::memcpy(dp.codebook, Wq->codebook, sizeof(dp.codebook));
-  dp.scales = ad->s;
-  dp.groups = &v.head->groups;
-  dp.grp_adapter = v.grp_adapter;
-  dp.grp_start = v.grp_start;
-  dp.grp_end = v.grp_end;
-  dp.perm = v.perm;
-  dp.owner = v.owner;
-  const int64_t grid = dp.units < sm_count() ? dp.units : sm_count();
-  auto launch = [&](auto kernel, int threads) {
+  if (M <= kDecodeMMax) {
+    if (!map_u8(&mc, Wq->codes, h / 2, o, h / 2, SD_UNIT_K / 2, SK_BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map_bf16_3d(&mx, X, 64, h / 64, M, 128, h * 2, 64, SD_UNIT_BLOCKS, static_cast<uint32_t>(M)))
+      return QLORA_ERR_CUDA;
+    DecodeParams dp{};
+    dp.M = static_cast<int>(M);
+    dp.N = static_cast<int>(o);
+    dp.k_units = static_cast<int>(div_up(h, SD_UNIT_K));
+    dp.blocks_per_row = static_cast<int>(h / 64);
+    dp.units = div_up(o, SK_BN) * dp.k_units;
+    dp.slot_bytes = static_cast<int>(div_up(SD_CODE_BYTES + M * SD_UNIT_BLOCKS * SD_X_ROW_BYTES, 1024) * 1024);
+    dp.low_bytes = SD_BAR_BYTES;
+    dp.r = r;
+    dp.P = w.PT;
+    dp.n_part = shrink_splits(M, ad->n, h);
+    dp.T_out = w.Tsum;
+    dp.absmax_fp8 = Wq->absmax_fp8;
+    dp.dq_scale = Wq->dq_scale;
+    dp.dq_mean = Wq->dq_mean;
+    dp.absmax32 = Wq->absmax;
+    dp.out = acc;
+    std::memcpy(dp.codebook, Wq->codebook, sizeof(dp.codebook));
+    auto kernel = M <= 8 ? small_m_mma_kernel<1, false> : small_m_mma_kernel<2, false>;
     if (set_smem(kernel, SD_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
     LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = SD_SMEM_BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, mc, mx, dp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-  };
-  const int lc = M <= 8    ? launch(small_m_mma_kernel<1, true>, sd_threads(1))
-                 : M <= 16 ? launch(small_m_mma_kernel<2, true>, sd_threads(2))
-                           : launch(small_m_mma_kernel<4, true>, sd_threads(4));
-  if (lc != QLORA_OK) return lc;
-  if (y_dtype == QLORA_DTYPE_BF16) {
-    LaunchScope ls(QLORA_KERNEL_AUX, st);
-    f32_to_bf16_kernel<<<static_cast<unsigned>(grid_for(M * o, 256, sm_count() * 4)), 256, 0, st>>>(
-        acc, M * o, static_cast<uint16_t*>(Y));
+    rc = launch_dependent(kernel, dim3(static_cast<unsigned>(dp.units < sm_count() ? dp.units : sm_count())), SD_THREADS,
+                          SD_SMEM_BYTES, st, mc, mx, dp);
+  } else {
+    const int nmma = static_cast<int>(div_up(M, 16) * 16);
+    if (!map_bf16(&mx, X, h, M, h * 2, 64, static_cast<uint32_t>(nmma)) ||
+        !map_u8(&mc, Wq->codes, h / 2, o, h / 2, 32, SK_BN, CU_TENSOR_MAP_SWIZZLE_32B))
+      return QLORA_ERR_CUDA;
+    SmallMParams sp{};
+    sp.M = static_cast<int>(M);
+    sp.N = static_cast<int>(o);
+    sp.nmma = nmma;
+    sp.k_units = static_cast<int>(h / SK_BK);
+    sp.ext_units = 0;
+    sp.blocks_per_row = static_cast<int>(h / 64);
+    sp.units = div_up(o, SK_BN) * sp.k_units;
+    sp.absmax_fp8 = Wq->absmax_fp8;
+    sp.dq_scale = Wq->dq_scale;
+    sp.dq_mean = Wq->dq_mean;
+    sp.absmax32 = Wq->absmax;
+    sp.out = acc;
+    std::memcpy(sp.codebook, Wq->codebook, sizeof(sp.codebook));
+    if (set_smem(small_m_fwd_kernel, SK_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+    LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
+    small_m_fwd_kernel<<<static_cast<unsigned>(sp.units < sm_count() ? sp.units : sm_count()), SK_THREADS,
+                         SK_SMEM_BYTES, st>>>(mx, mc, mx, mx, sp);
+    rc = launch_status();
   }
-  return launch_status();
+  if (rc != QLORA_OK) return rc;
+  ExpandParams ep{};
+  ep.P = M <= kDecodeMMax ? w.Tsum : w.PT;
+  ep.L2 = static_cast<const uint16_t*>(ad->L2);
+  ep.s = ad->s;
+  ep.acc = acc;
+  ep.Y = Y;
+  ep.T = T_save;
+  ep.parts = M <= kDecodeMMax ? 1 : shrink_splits(M, ad->n, h);
+  ep.r = r;
+  ep.N = static_cast<int>(o);
+  ep.max_groups = static_cast<int>(ad->n < M ? ad->n : M);
+  const dim3 grid(static_cast<unsigned>(div_up(o, MX_COLS)), static_cast<unsigned>(ep.max_groups + 1));
+  LaunchScope ls(QLORA_KERNEL_TGEMM, st);
+  return y_dtype == QLORA_DTYPE_BF16 ? launch_dependent(multi_expand_kernel<true>, grid, MX_THREADS, 0, st, ep, v)
+                                     : launch_dependent(multi_expand_kernel<false>, grid, MX_THREADS, 0, st, ep, v);
 }
 
 int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlora_adapters_t* ad, int64_t o,

@@ -15,7 +15,7 @@ from typing import Callable, Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
 
-from ._lib import (QLORA_DTYPE_BF16, QLORA_DTYPE_F32, _check, _stream, lib, qlora_adamw_state_t, qlora_adamw_t,
+from ._lib import (QLORA_DTYPE_BF16, QLORA_DTYPE_F32, _call, _check, _stream, lib, qlora_adamw_state_t, qlora_adamw_t,
                    qlora_adamw_tensor_t)
 from .paged import AdamWConfig, ManagedBuffer, PagingPolicy
 
@@ -156,13 +156,12 @@ class MultiAdamW:
         ptrs = (ctypes.c_uint64 * len(found)).from_buffer(array.array("Q", found))
         if self._buffers and (self.watermark > 0 or self.policy.on_host):
             self.policy.on_step()
-        c, dev = self.cfg, self.device
+        c = self.cfg
         hp = qlora_adamw_t(c.lr, c.beta1, c.beta2, c.eps, c.weight_decay, float(c.max_grad_norm or 0.0), 0)
-        with torch.cuda.device(dev):
-            _check(lib().qlora_multi_adamw_step(
-                ctypes.c_void_p(self._plan.data_ptr()), self._plan.numel(), len(self._numel), self._elems, ptrs,
-                QLORA_DTYPE_F32 if torch.float32 in dtypes else QLORA_DTYPE_BF16, ctypes.byref(self._struct),
-                ctypes.byref(hp), _stream(dev)), "qlora_multi_adamw_step")
+        _call(lib().qlora_multi_adamw_step, "qlora_multi_adamw_step", self.device, self._plan.data_ptr(),
+              self._plan.numel(), len(found), self._elems, ptrs,
+              QLORA_DTYPE_F32 if torch.float32 in dtypes else QLORA_DTYPE_BF16, ctypes.byref(self._struct),
+              ctypes.byref(hp))
 
     def moments(self, i: int) -> Tuple[torch.Tensor, torch.Tensor]:
         """m and v of tensor i in fp32, shaped like it, decoded from 8 bits where they are held so."""
