@@ -636,6 +636,7 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorM
 
 struct MultiPairParams {
   PairGemmParams g;         // k_ext_stages is not used: a tile has chunks stages per slot
+  int even;                 // no whole rounds: the stages of all tiles in even shares (see below)
   int chunks;               // rp / 64
   int rp, parts;
   const uint16_t* A;        // [M][K], batch order
@@ -669,6 +670,95 @@ __device__ __noinline__ float multi_element(const MultiPairParams& p, const Plan
   return x;
 }
 
+// Whether rows of several owners (groups, or none) meet in a 256-row tile.
+__device__ __forceinline__ bool tile_shared(const MultiPairParams& p, const PlanView& v, int mt) {
+  const int s0 = v.tile_slot0[mt], ns = v.tile_slot0[mt + 1] - s0;
+  if (ns != 1) return ns > 1;
+  const int g = v.slot_group[s0];
+  return v.grp_start[g] > mt * PG_BM || v.grp_end[g] < min((mt + 1) * PG_BM, p.g.M);
+}
+
+// Replaces what is not finite among the elements n .. n + kN - 1 of sorted row m by its own sum.
+template <bool kBwd, int kN>
+__device__ __forceinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, float* x) {
+  // x 0 is 0 for finite x: one fused multiply-add each finds what is not
+  float z = 0.0f;
+#pragma unroll
+  for (int t = 0; t < kN; ++t) z = fmaf(x[t], 0.0f, z);
+  if (z == 0.0f) return;
+  for (int t = 0; t < kN; ++t) {
+    float y = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kN; ++u) y = u == t ? x[u] : y;
+    if (isfinite(y)) continue;
+    y = multi_element<kBwd>(p, v, m, n + t);
+#pragma unroll
+    for (int u = 0; u < kN; ++u) x[u] = u == t ? y : x[u];
+  }
+}
+
+// Fewer tiles than SM pairs (`even`): the K stages of all tiles, one tile after
+// the other, are dealt out in equal contiguous shares, so that every pair works
+// for the same time whatever the number of tiles and of slots in them (333
+// tokens, 13824 x 5120: 40 tiles on 74 pairs, 99 us with one tile a pair,
+// EVEN333).  A share's first and last tile may be partial: their sums go to
+// the pair's two places of the partial buffer, and multi_reduce_kernel adds
+// the places of a tile in order.
+struct StageShare {
+  int64_t lo, hi;  // stages of this pair
+};
+__device__ __forceinline__ StageShare stage_share(int64_t total, int pair, int pairs) {
+  return {total * pair / pairs, total * (pair + 1) / pairs};
+}
+
+struct PairTiles {
+  int m_tiles, n_tiles;
+  __device__ __forceinline__ void at(int u, int& mt, int& n0) const {
+    const int band = u / (PG_BAND * m_tiles);
+    const int r = u - band * PG_BAND * m_tiles;
+    const int width = min(PG_BAND, n_tiles - band * PG_BAND);
+    mt = r / width;
+    n0 = (band * PG_BAND + r % width) * PG_BN;
+  }
+};
+
+// Stages of tile u.
+__device__ __forceinline__ int tile_stages(const MultiPairParams& p, const PlanView& v, int u) {
+  const PairTiles tiles{p.g.units / p.g.n_tiles, p.g.n_tiles};
+  int mt, n0;
+  tiles.at(u, mt, n0);
+  return p.g.k_main_stages + (v.tile_slot0[mt + 1] - v.tile_slot0[mt]) * p.chunks;
+}
+
+// Calls f(u, first stage, stages) for all tiles, by one warp; returns the sum of the stages.
+template <typename F>
+__device__ __forceinline__ int64_t walk_tiles(const MultiPairParams& p, const PlanView& v, F f) {
+  const int lane = threadIdx.x & 31;
+  int64_t carry = 0;
+  for (int b = 0; b < p.g.units; b += 32) {
+    const int u = b + lane;
+    const int n = u < p.g.units ? tile_stages(p, v, u) : 0;
+    int s = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += x;
+    }
+    f(u, carry + s - n, n);
+    carry += __shfl_sync(0xFFFFFFFFu, s, 31);
+  }
+  return carry;
+}
+
+// A piece of a tile that a pair computes.
+struct PairItem {
+  int mt, n0, kbeg, kend;
+  int slot0;  // first slot of the tile
+  int part;   // place in the partial buffer (-1: the whole tile)
+};
+constexpr int MG_PAIR_ITEMS = 128;  // pieces of an even share: at most the tiles, which are fewer than the pairs
+constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<int>(sizeof(PairItem));
+
 // pair_gemm_kernel's pipeline (256 x 256 tiles on two-SM clusters, 128-deep
 // stages, two accumulators, K parts for what does not fill a round) with K
 // extended per tile: one stage for every slot of the tile and 64 ranks, A the
@@ -691,6 +781,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   uint64_t* tfull = empty + PG_STAGES;   // each CTA: accumulator complete
   uint64_t* tempty = tfull + 2;          // even CTA: the 8 epilogue warps of the pair
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  int* n_even = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + PG_BAR_BYTES);
+  PairItem* even = reinterpret_cast<PairItem*>(n_even + 4);
 
   const PairGemmParams& p = mp.g;
   const uint32_t rank = cluster_ctarank();
@@ -699,27 +791,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int KM = p.k_main_stages;
-  const int m_tiles = p.units / p.n_tiles;
-  auto tile_of = [&](int u, int& mt, int& n0) {
-    const int band = u / (PG_BAND * m_tiles);
-    const int r = u - band * PG_BAND * m_tiles;
-    const int width = min(PG_BAND, p.n_tiles - band * PG_BAND);
-    mt = r / width;
-    n0 = (band * PG_BAND + r % width) * PG_BN;
-  };
+  const PairTiles tiles{p.units / p.n_tiles, p.n_tiles};
   const int n_parts = (p.units - p.full_units) * p.split;
   const int n_items = p.full_units + n_parts;
-  const int nk = pair < n_items ? (n_items - 1 - pair) / npairs + 1 : 0;  // items of this pair
-  struct Item {
-    int mt, n0, kbeg, kend;
-    int slot0;  // first slot of the tile
-    int part;   // index of a split part (-1: a whole tile)
-  };
-  auto item_of = [&](int k) -> Item {
+  auto item_of = [&](int k) -> PairItem {
+    if (mp.even) return even[k];
     const int u = pair + k * npairs;
-    Item it;
+    PairItem it;
     it.part = u >= n_parts ? -1 : u;
-    tile_of(u >= n_parts ? u - n_parts : p.full_units + u / p.split, it.mt, it.n0);
+    tiles.at(u >= n_parts ? u - n_parts : p.full_units + u / p.split, it.mt, it.n0);
     it.slot0 = v.tile_slot0[it.mt];
     const int S = KM + (v.tile_slot0[it.mt + 1] - it.slot0) * mp.chunks;
     it.kbeg = 0;
@@ -731,6 +811,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
     }
     return it;
   };
+  if (mp.even && warp == 2) {
+    const int64_t total = walk_tiles(mp, v, [](int, int64_t, int) {});
+    const StageShare share = stage_share(total, pair, npairs);
+    int count = 0;
+    walk_tiles(mp, v, [&](int u, int64_t at, int n) {
+      const bool mine = n > 0 && at < share.hi && at + n > share.lo;
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
+      if (mine) {
+        const int k = count + __popc(who & ((1u << lane) - 1u));
+        PairItem it;
+        tiles.at(u, it.mt, it.n0);
+        it.kbeg = static_cast<int>(max(share.lo - at, static_cast<int64_t>(0)));
+        it.kend = static_cast<int>(min(share.hi - at, static_cast<int64_t>(n)));
+        it.slot0 = v.tile_slot0[it.mt];
+        it.part = it.kbeg == 0 && it.kend == n ? -1 : 2 * pair + (at > share.lo ? 1 : 0);
+        even[k] = it;
+      }
+      count += __popc(who);
+    });
+    if (lane == 0) *n_even = count;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < PG_STAGES; ++s) {
@@ -754,6 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   cluster_barrier();  // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int nk = mp.even ? *n_even : (pair < n_items ? (n_items - 1 - pair) / npairs + 1 : 0);  // items of this pair
 
   if (warp == 0) {
     if (lane == 0) {
@@ -762,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
       int G = 0;
       bool ok = true;
       for (int k = 0; k < nk && ok; ++k) {
-        const Item it = item_of(k);
+        const PairItem it = item_of(k);
         const int m0 = it.mt * PG_BM + static_cast<int>(rank) * 128;
         const int n0 = it.n0 + static_cast<int>(rank) * 128;
         for (int i = it.kbeg; i < it.kend; ++i, ++G) {
@@ -829,7 +931,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
         if (!mbar_wait_idle<true>(&tempty[b], ((k >> 1) & 1) ^ 1, kTagPgTEmpty)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem + static_cast<uint32_t>(b * PG_ACC_COLS);
-        const Item it = item_of(k);
+        const PairItem it = item_of(k);
         for (int i = it.kbeg; i < it.kend; ++i, ++G) {
           const int s = G % PG_STAGES;
           if (!mbar_wait(&full[s], (G / PG_STAGES) & 1, kTagPgFull)) {
@@ -859,22 +961,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
     const int q = warp & 3;
     auto store_row = [&](int m, int64_t row, int n, float* x, bool shared) {
       if (m >= p.M || n >= p.N) return;
-      if (shared) {
-        // x 0 is 0 for finite x: one fused multiply-add each finds what is not
-        float z = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) z = fmaf(x[t], 0.0f, z);
-        if (z != 0.0f)
-          for (int t = 0; t < 16; ++t) {
-            float y = 0.0f;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) y = u == t ? x[u] : y;
-            if (isfinite(y)) continue;
-            y = multi_element<kBwd>(mp, v, m, n + t);
-#pragma unroll
-            for (int u = 0; u < 16; ++u) x[u] = u == t ? y : x[u];
-          }
-      }
+      if (shared) multi_repair<kBwd, 16>(mp, v, m, n, x);
       if (p.out_bf16) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.ld_out + n);
         uint32_t h[8];
@@ -892,17 +979,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
       const int b = k & 1;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_idle(&tfull[b], (k >> 1) & 1, kTagPgTFull))) break;
       tc_fence_after();
-      const Item it = item_of(k);
+      const PairItem it = item_of(k);
       const int row = static_cast<int>(rank) * 128 + q * 32 + lane;  // row within the pair tile
       const int m = it.mt * PG_BM + row;
       const int64_t to = m < p.M ? v.perm[m] : 0;
-      // whether rows of several owners (groups, or none) meet in the tile
-      const int ns = v.tile_slot0[it.mt + 1] - it.slot0;
-      bool shared = ns > 1;
-      if (ns == 1) {
-        const int g = v.slot_group[it.slot0];
-        shared = v.grp_start[g] > it.mt * PG_BM || v.grp_end[g] < min((it.mt + 1) * PG_BM, p.M);
-      }
+      const bool shared = tile_shared(mp, v, it.mt);
       float* part = it.part >= 0 ? p.partial + (static_cast<int64_t>(it.part) * PG_BM + row) * PG_BN : nullptr;
 #pragma unroll 1
       for (int c = 0; c < PG_ACC_COLS / 16; ++c) {
@@ -919,13 +1000,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
         for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(r[t]);
         if (part) {
           float4* dst = reinterpret_cast<float4*>(part + c * 16);
+          if (m < p.M)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
+            for (int t = 0; t < 4; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
         } else {
           store_row(m, to, it.n0 + c * 16, x, shared);
         }
       }
-      if (part) {
+      if (part && !mp.even) {
         // the warp that completes the last part of a tile sums the parts in order
         __threadfence();
         __syncwarp();
@@ -965,6 +1047,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 2 * PG_ACC_COLS);
+  }
+}
+
+// Adds the partial sums of the tiles that several pairs computed, in the order
+// of their stages.  blockIdx.x: tile, blockIdx.y: 16 of its rows.
+constexpr int MR_ROWS = 16;
+template <bool kBwd>
+__global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant__ MultiPairParams mp, int pairs,
+                                                           const __grid_constant__ PlanView v) {
+  __shared__ int64_t at, all;
+  __shared__ int len;
+  const PairGemmParams& p = mp.g;
+  const int u = blockIdx.x;
+  int mt, n0;
+  PairTiles{p.units / p.n_tiles, p.n_tiles}.at(u, mt, n0);
+  const int m0 = mt * PG_BM + MR_ROWS * static_cast<int>(blockIdx.y);
+  if (m0 >= p.M) return;
+  if (threadIdx.x < 32) {
+    const int64_t total = walk_tiles(mp, v, [&](int t, int64_t first, int n) {
+      if (t == u) at = first, len = n;
+    });
+    if (threadIdx.x == 0) all = total;
+  }
+  __syncthreads();
+  // the first and last pair with stages of this tile, and the place of the first's sum
+  int c0 = static_cast<int>(at * pairs / all);
+  while (stage_share(all, c0, pairs).hi <= at) ++c0;
+  while (c0 > 0 && stage_share(all, c0, pairs).lo > at) --c0;
+  int c1 = c0;
+  while (stage_share(all, c1, pairs).hi < at + len) ++c1;
+  if (c0 == c1) return;  // one pair computed the whole tile and has stored it
+  const int64_t place0 = 2 * c0 + (at > stage_share(all, c0, pairs).lo ? 1 : 0);
+  const bool shared = tile_shared(mp, v, mt);
+  for (int q = threadIdx.x; q < MR_ROWS * PG_BN / 4; q += 256) {
+    const int m = m0 + q / (PG_BN / 4), c = 4 * (q % (PG_BN / 4));
+    if (m >= p.M || n0 + c >= p.N) continue;
+    const int64_t off = static_cast<int64_t>(m - mt * PG_BM) * PG_BN + c;
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.partial + place0 * PG_BM * PG_BN + off));
+    float x[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll 4
+    for (int k = c0 + 1; k <= c1; ++k) {  // the tile is the first of every further pair's share
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.partial + static_cast<int64_t>(2 * k) * PG_BM * PG_BN + off));
+      x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
+    }
+    if (shared) multi_repair<kBwd, 4>(mp, v, m, n0 + c, x);
+    const int64_t to = static_cast<int64_t>(v.perm[m]) * p.ld_out + n0 + c;
+    if (p.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
+          make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 

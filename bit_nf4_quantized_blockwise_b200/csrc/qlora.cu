@@ -1557,7 +1557,9 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
     w.SU = static_cast<uint16_t*>(take(slot_bytes));
   }
   w.Wd = static_cast<uint16_t*>(take(o * h * 2));
-  w.Wpart = static_cast<float*>(take(pairs * PG_BM * PG_BN * 4));
+  // partial sums: a place for every pair, two where the pairs share all tiles evenly
+  const int64_t units = div_up(M, PG_BM) * div_up(bwd ? h : o, PG_BN);
+  w.Wpart = static_cast<float*>(take((units < pairs ? 2 : 1) * pairs * PG_BM * PG_BN * 4));
   w.Wcnt = static_cast<unsigned*>(take(pairs * 8 * 4));
   w.bytes = off;
   return w;
@@ -1635,7 +1637,7 @@ int multi_resident_pairs() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>((sm_count() + 1) / 2), 1, 1);
   cfg.blockDim = dim3(PG_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = PG_SMEM_BYTES;
+  cfg.dynamicSmemBytes = MG_PAIR_SMEM;
   if (cudaOccupancyMaxActiveClusters(&n, multi_pair_kernel<kBwd>, &cfg) != cudaSuccess || n <= 0) return 0;
   cache[dev].store(n);
   return n;
@@ -1655,7 +1657,7 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   if (kBwd ? !map_bf16_3d(&mbe, ad->L1, r, h, ad->n, r * 2, h * r * 2, 64, 128, 1)
            : !map_bf16_3d(&mbe, ad->L2, o, r, ad->n, o * 2, r * o * 2, 64, 64, 1))
     return QLORA_ERR_CUDA;
-  if (set_smem(multi_pair_kernel<kBwd>, PG_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (set_smem(multi_pair_kernel<kBwd>, MG_PAIR_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
   int pairs = multi_resident_pairs<kBwd>();
   if (pairs <= 0) return QLORA_ERR_CUDA;
   if (pairs > (sm_count() + 1) / 2) pairs = (sm_count() + 1) / 2;  // the partial buffer's bound
@@ -1668,13 +1670,12 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.out = out;
   p.g.out_bf16 = out_bf16;
   p.g.ld_out = N;
-  // The tiles of the last round, which would leave pairs without work, are split along K, each
-  // part at least two stages deep; up to four parts a tile beside whole tiles, up to eight when
-  // there are none (a batch of a few tokens).
-  const int tail = p.g.units % pairs;
-  const int most = p.g.units < pairs ? 8 : 4;
+  p.even = p.g.units < pairs ? 1 : 0;
+  // With whole rounds, the tiles of the last one, which would leave pairs without work, are split
+  // along K into up to four parts (each at least two stages) that run first.
+  const int tail = p.even ? 0 : p.g.units % pairs;
   int split = tail > 0 ? pairs / tail : 1;
-  if (split > most) split = most;
+  if (split > 4) split = 4;
   if (split > p.g.k_main_stages / 2) split = p.g.k_main_stages / 2;
   if (split < 2) split = 1;
   p.g.split = split;
@@ -1692,11 +1693,18 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.r = ad->r;
   if (split > 1 && cudaMemsetAsync(w.Wcnt, 0, static_cast<size_t>(tail) * 8 * 4, st) != cudaSuccess)
     return QLORA_ERR_CUDA;
-  const int items = p.g.full_units + (p.g.units - p.g.full_units) * split;
-  const int clusters = items < pairs ? items : pairs;
+  // even shares: a pair for every two main stages, as far as there are pairs
+  const int64_t most = static_cast<int64_t>(p.g.units) * p.g.k_main_stages / 2;
+  const int clusters = !p.even || most >= pairs ? pairs : static_cast<int>(most > 1 ? most : 1);
   {
     LaunchScope ls(kBwd ? QLORA_KERNEL_FUSED_BWD : QLORA_KERNEL_FUSED_FWD, st);
-    multi_pair_kernel<kBwd><<<2 * clusters, PG_THREADS, PG_SMEM_BYTES, st>>>(ma, mas, mb, mae, mbe, p, v);
+    multi_pair_kernel<kBwd><<<2 * clusters, PG_THREADS, MG_PAIR_SMEM, st>>>(ma, mas, mb, mae, mbe, p, v);
+  }
+  if (p.even && clusters > 1) {
+    const int64_t rows = M < PG_BM ? M : PG_BM;
+    LaunchScope ls(QLORA_KERNEL_AUX, st);
+    multi_reduce_kernel<kBwd><<<dim3(static_cast<unsigned>(p.g.units), static_cast<unsigned>(div_up(rows, MR_ROWS))),
+                                256, 0, st>>>(p, clusters, v);
   }
   return launch_status();
 }
