@@ -454,8 +454,9 @@ __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, con
       const int64_t orig = v.perm[at];
       if (job.P) {
         const float* src = job.P + static_cast<int64_t>(at) * p.r + c;
+#pragma unroll 4
         for (int k = 0; k < job.splits; ++k) {
-          const float4 f = *reinterpret_cast<const float4*>(src + k * part);
+          const float4 f = __ldg(reinterpret_cast<const float4*>(src + k * part));
           x[0] += f.x, x[1] += f.y, x[2] += f.z, x[3] += f.w;
         }
       } else {
@@ -1104,20 +1105,32 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
 // ====================================================================== gradients of the factors
 
 // dL1[a] = X_a^T (s U_a) and dL2[a]^T = dY_a^T (s T_a) over the rows of group a:
-// D is 128 rows of h (or o) by the ranks, K runs over the group's 64-row blocks
+// D is 128 rows of h (or o) by 64 ranks, K runs over the group's 64-row blocks
 // of the sorted order, A from X (or dY) as it lies (M-major), B the slots' three
-// bf16 parts (N-major), three MMAs a step into one accumulator.  The slots are
-// zero in the rows of a block that belong to others.  One CTA adds all tokens of
-// its tile in order and stores them, so the gradients do not depend on timing;
-// adapters without tokens get zeros.  blockIdx.x: tiles of dL1, then of dL2;
-// blockIdx.y: adapter.
+// bf16 parts side by side (N-major, N = 192): each part has accumulator columns
+// of its own, added in fp32 at the end, so the rounding of the two small parts'
+// sums does not count and the first part's chain is a third as long (4096 tokens
+// in 4 groups: error against fp64 GRADERR).  The slots are zero in the rows of a
+// block that belong to others.
+// A group's blocks are dealt to the `split` CTAs of a cluster, whose sums are
+// added in order through distributed shared memory: groups differ in length, a
+// tile's time is its longest group's, and two stages in flight a CTA cover an L2
+// latency only with several CTAs on a group.  No sum depends on timing; adapters
+// without tokens get zeros.  blockIdx.x: the CTAs of each tile of dL1, then of
+// dL2; blockIdx.y: adapter.
 constexpr int MD_BM = 128;
+constexpr int MD_BN = 64;
 constexpr int MD_BK = 64;
 constexpr int MD_THREADS = 128;
-constexpr int MD_A_BYTES = MD_BM * MD_BK * 2;
-constexpr int MD_MAX_STAGES = 4;
-constexpr int MD_SMEM_LIMIT = 110 * 1024;  // two CTAs an SM
 constexpr int MD_PARTS = 3;
+constexpr int MD_A_BYTES = MD_BM * MD_BK * 2;
+constexpr int MD_B_BYTES = MD_BN * MD_BK * 2;
+constexpr int MD_STAGE_BYTES = MD_A_BYTES + MD_PARTS * MD_B_BYTES;
+constexpr int MD_STAGES = 2;               // two CTAs an SM
+constexpr int MD_SUM_PITCH = MD_BN + 4;    // floats a row of the CTA's sums (over the ring)
+constexpr int MD_SMEM = MD_STAGES * MD_STAGE_BYTES + 1024 + 128;
+constexpr uint32_t MD_TMEM_COLS = 256;     // 192 used
+static_assert(MD_BM * MD_SUM_PITCH * 4 <= MD_STAGES * MD_STAGE_BYTES, "the sums fit the ring");
 
 struct MultiGradSide {
   const uint16_t* A;      // X or dY, batch order
@@ -1128,63 +1141,79 @@ struct MultiGradSide {
 
 struct MultiGradParams {
   MultiGradSide side[2];
-  int r, rp, bn, stages;
+  int r, rp;
   int tiles0;  // 128-row tiles of dL1, times the rank tiles
 };
 
-__global__ void __launch_bounds__(MD_THREADS, 1)
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// One element of a factor's gradient from the group's own tokens alone, in fp32.
+__device__ __noinline__ float grad_element(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j) {
+  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp], slot0 = v.grp_slot0[grp];
+  float y = 0.0f;
+  for (int row = g0; row < g1; ++row) {
+    const int64_t slot_row = static_cast<int64_t>(slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS +
+                             row % MP_SLOT_ROWS;
+    const uint16_t* b = side.slots + slot_row * (MD_PARTS * rp) + j;
+    const float w = bf16_bits_to_float(b[0]) + bf16_bits_to_float(b[rp]) + bf16_bits_to_float(b[2 * rp]);
+    y = fmaf(bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]), w, y);
+  }
+  return y;
+}
+
+template <int kSplit>
+__global__ void __launch_bounds__(MD_THREADS, 2)
     multi_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                       const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDs,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmT,
                       const __grid_constant__ MultiGradParams p, const __grid_constant__ PlanView v) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int b_bytes = p.bn * MD_BK * 2;
-  const int stage_bytes = MD_A_BYTES + MD_PARTS * b_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
-  uint64_t* empty = full + MD_MAX_STAGES;
-  uint64_t* accum = empty + MD_MAX_STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + MD_STAGES * MD_STAGE_BYTES);
+  uint64_t* empty = full + MD_STAGES;
+  uint64_t* accum = empty + MD_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+  float* sums = reinterpret_cast<float*>(smem);  // [128][MD_SUM_PITCH], once the ring is done with
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int second = static_cast<int>(blockIdx.x) >= p.tiles0 ? 1 : 0;
+  const int index = static_cast<int>(blockIdx.x) / kSplit, part = static_cast<int>(blockIdx.x) % kSplit;
+  const int second = index >= p.tiles0 ? 1 : 0;
   const MultiGradSide side = second ? p.side[1] : p.side[0];
-  const int n_tiles = p.rp / p.bn;
-  const int tile = static_cast<int>(blockIdx.x) - (second ? p.tiles0 : 0);
+  const int n_tiles = p.rp / MD_BN;
+  const int tile = index - (second ? p.tiles0 : 0);
   const int m0 = (tile / n_tiles) * MD_BM;
-  const int j0 = (tile % n_tiles) * p.bn;
+  const int j0 = (tile % n_tiles) * MD_BN;
   const int adapter = blockIdx.y;
   const int grp = v.adp_group[adapter];
   float* out = side.out + static_cast<int64_t>(adapter) * p.r * side.rows;
-  const int m = m0 + threadIdx.x;
-  auto store = [&](int n, const float* x) {  // 16 ranks n .. n + 15 of row m
-    if (m >= side.rows) return;
-#pragma unroll
-    for (int t = 0; t < 16; t += 4) {
-      if (n + t >= p.r) return;
-      if (second) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) out[static_cast<int64_t>(n + t + u) * side.rows + m] = x[t + u];
-      } else {
-        *reinterpret_cast<float4*>(out + static_cast<int64_t>(m) * p.r + n + t) =
-            make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
-      }
+  const int rows = min(MD_BM, side.rows - m0), ranks = min(MD_BN, p.r - j0);
+  // this CTA's share of the tile's rows of D
+  const int r0 = MD_BM * part / kSplit, r1 = min(rows, MD_BM * (part + 1) / kSplit);
+  if (grp < 0) {  // the same for the whole cluster
+    if (second) {
+      for (int q = threadIdx.x; q < (r1 - r0) * ranks; q += MD_THREADS)
+        out[static_cast<int64_t>(j0 + q / (r1 - r0)) * side.rows + m0 + r0 + q % (r1 - r0)] = 0.0f;
+    } else {
+      for (int q = threadIdx.x; q < (r1 - r0) * ranks; q += MD_THREADS)
+        out[static_cast<int64_t>(m0 + r0 + q / ranks) * p.r + j0 + q % ranks] = 0.0f;
     }
-  };
-  if (grp < 0) {
-    const float zero[16] = {};
-    for (int c = 0; c < p.bn; c += 16) store(j0 + c, zero);
     return;
   }
   const int g0 = v.grp_start[grp], g1 = v.grp_end[grp];
   const int blk0 = g0 / MD_BK;
-  const int S = (g1 - 1) / MD_BK - blk0 + 1;
+  const int blocks = (g1 - 1) / MD_BK - blk0 + 1;
+  const int i0 = blocks * part / kSplit;
+  const int S = blocks * (part + 1) / kSplit - i0;
   const int slot0 = v.grp_slot0[grp];
-  const uint32_t tmem_cols = p.bn <= 64 ? 64u : 128u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < MD_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -1192,7 +1221,7 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_alloc(tmem_slot, MD_TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -1205,87 +1234,104 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
     const CUtensorMap* mb = second ? &tmT : &tmU;
     int issued = 0;
     for (int i = 0; i < S; ++i) {
-      const int s = i % p.stages;
-      if (!mbar_wait(&empty[s], ((i / p.stages) & 1) ^ 1)) break;
-      uint8_t* st = smem + s * stage_bytes;
-      const int row = (blk0 + i) * MD_BK;
+      const int s = i % MD_STAGES;
+      if (!mbar_wait(&empty[s], ((i / MD_STAGES) & 1) ^ 1)) break;
+      uint8_t* st = smem + s * MD_STAGE_BYTES;
+      const int row = (blk0 + i0 + i) * MD_BK;
       // the block's rows within the group's slots
       const int y = (slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
-      mbar_arrive_expect_tx(&full[s], stage_bytes);
+      mbar_arrive_expect_tx(&full[s], MD_STAGE_BYTES);
       tma_load_2d(st, ma, &full[s], m0, row);
       tma_load_2d(st + MD_A_BYTES / 2, ma, &full[s], m0 + 64, row);
-      for (int h = 0; h < MD_PARTS; ++h)
-        for (int t = 0; t < p.bn / 64; ++t)
-          tma_load_2d(st + MD_A_BYTES + h * b_bytes + t * 8192, mb, &full[s], h * p.rp + j0 + 64 * t, y);
+      for (int h = 0; h < MD_PARTS; ++h) tma_load_2d(st + MD_A_BYTES + h * MD_B_BYTES, mb, &full[s], h * p.rp + j0, y);
       issued = i + 1;
     }
-    for (int i = issued - p.stages > 0 ? issued - p.stages : 0; i < issued; ++i)
-      mbar_wait(&full[i % p.stages], (i / p.stages) & 1);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16(MD_BM, p.bn, true, true);
+    for (int i = issued - MD_STAGES > 0 ? issued - MD_STAGES : 0; i < issued; ++i)
+      mbar_wait(&full[i % MD_STAGES], (i / MD_STAGES) & 1);
+  } else if (warp == 1 && lane == 0 && S > 0) {
+    const uint32_t idesc = idesc_bf16(MD_BM, MD_PARTS * MD_BN, true, true);
     for (int i = 0; i < S; ++i) {
-      const int s = i % p.stages;
-      if (!mbar_wait(&full[s], (i / p.stages) & 1)) break;
+      const int s = i % MD_STAGES;
+      if (!mbar_wait(&full[s], (i / MD_STAGES) & 1)) break;
       tc_fence_after();
-      const uint32_t a_base = smem_u32(smem + s * stage_bytes);
+      const uint32_t a_base = smem_u32(smem + s * MD_STAGE_BYTES);
 #pragma unroll
-      for (int kk = 0; kk < MD_BK / 16; ++kk) {
-        const uint64_t adesc = sw128_desc(a_base + kk * 2048, MD_A_BYTES / 2, 1024);
-#pragma unroll
-        for (int h = 0; h < MD_PARTS; ++h) {
-          const uint64_t bdesc = sw128_desc(a_base + MD_A_BYTES + h * b_bytes + kk * 2048, 8192, 1024);
-          umma_bf16(tmem, adesc, bdesc, idesc, (i > 0 || kk > 0 || h > 0) ? 1u : 0u);
-        }
-      }
+      for (int kk = 0; kk < MD_BK / 16; ++kk)
+        umma_bf16(tmem, sw128_desc(a_base + kk * 2048, MD_A_BYTES / 2, 1024),
+                  sw128_desc(a_base + MD_A_BYTES + kk * 2048, MD_B_BYTES, 1024), idesc, (i > 0 || kk > 0) ? 1u : 0u);
       umma_commit(&empty[s]);
     }
     umma_commit(accum);
   }
 
   __syncwarp();
-  const bool ok = mbar_wait(accum, 0);
+  const bool ok = S == 0 || mbar_wait(accum, 0);
   tc_fence_after();
-  if (ok) {
-    // rows of others in the group's first or last block
-    const bool shared = g0 % MD_BK != 0 || (g1 % MD_BK != 0 && g1 < v.M);
-    for (int c = 0; c < p.bn; c += 16) {
-      uint32_t r[16];
-      tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
-      tmem_ld_wait();
+  __syncthreads();  // the ring is free: every copy has landed (the producer waited) and every MMA is done
+  {
+    float* row = sums + threadIdx.x * MD_SUM_PITCH;
+    for (int c = 0; c < MD_BN; c += 16) {
       float x[16];
-      float z = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        x[t] = __uint_as_float(r[t]);
-        z = fmaf(x[t], 0.0f, z);
+      for (int t = 0; t < 16; ++t) x[t] = 0.0f;
+      if (S > 0 && ok) {
+        uint32_t a[16], b[16], d[16];
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
+        tmem_ld16(at, a);
+        tmem_ld16(at + MD_BN, b);
+        tmem_ld16(at + 2 * MD_BN, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+          x[t] = __uint_as_float(a[t]) + (__uint_as_float(b[t]) + __uint_as_float(d[t]));
       }
-      if (shared && z != 0.0f && m < side.rows) {
-        for (int t = 0; t < 16; ++t) {
-          if (j0 + c + t >= p.r) break;
-          float y = 0.0f;
 #pragma unroll
-          for (int u = 0; u < 16; ++u) y = u == t ? x[u] : y;
-          if (isfinite(y)) continue;
-          y = 0.0f;
-          for (int row = g0; row < g1; ++row) {
-            const uint16_t* b = side.slots + (static_cast<int64_t>(slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) *
-                                                  MP_SLOT_ROWS + row % MP_SLOT_ROWS) * (MD_PARTS * p.rp) + j0 + c + t;
-            const float w = bf16_bits_to_float(b[0]) + bf16_bits_to_float(b[p.rp]) + bf16_bits_to_float(b[2 * p.rp]);
-            y = fmaf(bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]), w, y);
-          }
-#pragma unroll
-          for (int u = 0; u < 16; ++u) x[u] = u == t ? y : x[u];
-        }
-      }
-      store(j0 + c, x);
+      for (int t = 0; t < 16; t += 4)
+        *reinterpret_cast<float4*>(row + c + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (kSplit > 1)
+    cluster_barrier();  // the sums of all CTAs are in shared memory
+  else
+    __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols);
+    tmem_dealloc(tmem, MD_TMEM_COLS);
   }
+  // rows of others in the group's first or last block
+  const bool shared = g0 % MD_BK != 0 || (g1 % MD_BK != 0 && g1 < v.M);
+  // four ranks of a row a thread; for dL2 neighbouring threads take neighbouring rows
+  constexpr int kRows = MD_BM / kSplit;
+  constexpr int kEach = kRows * (MD_BN / 4) / MD_THREADS;  // float4s a thread
+  auto row_of = [&](int q) { return r0 + (second ? q % kRows : q / (MD_BN / 4)); };
+  auto rank_of = [&](int q) { return 4 * (second ? q / kRows : q % (MD_BN / 4)); };
+#pragma unroll 1
+  for (int e = 0; e < kEach; ++e) {
+    const int q = threadIdx.x + e * MD_THREADS;
+    const int m = row_of(q), c = rank_of(q);
+    if (m >= r1 || c >= ranks) continue;
+    float* src = sums + m * MD_SUM_PITCH + c;
+    float4 f[kSplit];  // all loads before the first sum: a remote one takes most of a microsecond
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k)
+      f[k] = kSplit == 1 ? *reinterpret_cast<const float4*>(src) : ld_cluster_v4(cluster_addr(src, static_cast<uint32_t>(k)));
+    float x[4] = {f[0].x, f[0].y, f[0].z, f[0].w};
+#pragma unroll
+    for (int k = 1; k < kSplit; ++k) x[0] += f[k].x, x[1] += f[k].y, x[2] += f[k].z, x[3] += f[k].w;
+    if (shared) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (!isfinite(x[t])) x[t] = grad_element(side, v, grp, p.rp, m0 + m, j0 + c + t);
+    }
+    if (second) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) out[static_cast<int64_t>(j0 + c + t) * side.rows + m0 + m] = x[t];
+    } else {
+      *reinterpret_cast<float4*>(out + static_cast<int64_t>(m0 + m) * p.r + j0 + c) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+  if (kSplit > 1) cluster_barrier();  // no CTA leaves while another still reads its sums
 }
 
 }  // namespace qlora

@@ -1819,22 +1819,34 @@ int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlo
   p.side[1] = {static_cast<const uint16_t*>(dY), w.ST, dL2, static_cast<int>(o)};
   p.r = ad->r;
   p.rp = static_cast<int>(rp);
-  p.bn = rp % 128 == 0 ? 128 : 64;
-  const int stage_bytes = MD_A_BYTES + MD_PARTS * p.bn * MD_BK * 2;
-  p.stages = MD_SMEM_LIMIT / stage_bytes;
-  if (p.stages < 2) p.stages = TG_SMEM_LIMIT_ONE / stage_bytes;
-  if (p.stages > MD_MAX_STAGES) p.stages = MD_MAX_STAGES;
-  const int n_tiles = p.rp / p.bn;
+  const int n_tiles = p.rp / MD_BN;
   p.tiles0 = static_cast<int>(div_up(h, MD_BM)) * n_tiles;
   const int tiles = p.tiles0 + static_cast<int>(div_up(o, MD_BM)) * n_tiles;
-  const int smem = p.stages * stage_bytes + 1024 + 256;
-  if (set_smem(multi_grad_kernel, smem) != QLORA_OK) return QLORA_ERR_CUDA;
-  {
+  // CTAs on a group: as many as fill the GPU (two an SM) about once, up to eight
+  const int64_t items = static_cast<int64_t>(tiles) * (ad->n < M ? ad->n : M);
+  int split = 1;
+  while (split < 8 && items * split * 2 <= 3 * sm_count() && split * MD_BK < M) split *= 2;
+  auto launch = [&](auto kernel) {
+    if (set_smem(kernel, MD_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(ad->n));
+    cfg.blockDim = dim3(MD_THREADS);
+    cfg.dynamicSmemBytes = MD_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     LaunchScope ls(QLORA_KERNEL_TGEMM, st);
-    multi_grad_kernel<<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ad->n)), MD_THREADS, smem, st>>>(
-        mx, mxs, md, mds, mu, mt, p, v);
-  }
-  return launch_status();
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mxs, md, mds, mu, mt, p, v) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  };
+  return split == 1   ? launch(multi_grad_kernel<1>)
+         : split == 2 ? launch(multi_grad_kernel<2>)
+         : split == 4 ? launch(multi_grad_kernel<4>)
+                      : launch(multi_grad_kernel<8>);
 }
 
 int check_multi_args(const qlora_nf4_t* Wq, int64_t M, const qlora_adapters_t* ad, int dtype, const void* plan,
