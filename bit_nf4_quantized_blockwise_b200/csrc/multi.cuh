@@ -47,23 +47,43 @@ struct PlanHead {
   int tiles;     // 64-row tiles of the groups
 };
 
-// Arrays of a plan (device); lengths in brackets, G = min(n, M).
+// A group: its rows are the sorted positions start .. end - 1.
+struct PlanGroup {
+  int adapter, start, end;
+  int slot0;  // its first slot
+};
+struct PlanSlot {
+  int adapter, start, end;  // of the group
+  int tile;                 // 256-row tile
+};
+struct PlanTile {
+  int adapter, row0, rows;  // up to 64 rows of a group
+  int group;
+};
+
+// Arrays of a plan (device); lengths in brackets, G = min(n, M).  A kernel gets
+// what it needs of a group, slot or tile with one 16-byte load: chains of
+// dependent loads at the start of every block are most of what a small batch
+// costs.
 struct PlanView {
   PlanHead* head;
   int* perm;         // [M] row of the batch at sorted position p
   int* owner;        // [M] adapter of row i of the batch, -1: none
-  int* grp_adapter;  // [G]
-  int* grp_start;    // [G] sorted positions of a group: grp_start <= p < grp_end
-  int* grp_end;      // [G]
-  int* grp_slot0;    // [G + 1] first slot
-  int* grp_tile0;    // [G + 1] first 64-row tile
+  PlanGroup* groups; // [G]
   int* adp_group;    // [n] group of an adapter, -1: no tokens
-  int* slot_group;   // [slots]
-  int* slot_tile;    // [slots] 256-row tile
+  PlanSlot* slots;   // [slots]
   int* tile_slot0;   // [tiles + 1] first slot of a 256-row tile
+  PlanTile* tiles;   // [64-row tiles]
   int* counts;       // scratch: [32][n + 1], then [n + 1] each of first, total, start
   int M, n;
 };
+
+template <typename T>
+__device__ __forceinline__ T plan_load(const T* p) {
+  static_assert(sizeof(T) == 16, "one 16-byte load");
+  const int4 x = __ldg(reinterpret_cast<const int4*>(p));
+  return *reinterpret_cast<const T*>(&x);
+}
 
 // Sum over the block's threads before this one, and the total (x, y apart).
 __device__ __forceinline__ int2 block_scan(int2 v, int2 (&sh)[MP_WARPS], int2& total) {
@@ -150,9 +170,7 @@ __global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __r
       start[key] = carry.y + at.y;
       if (key < n) {
         const int g = carry.x + at.x;
-        v.grp_adapter[g] = key;
-        v.grp_start[g] = start[key];
-        v.grp_end[g] = start[key] + total[key];
+        v.groups[g] = {key, start[key], start[key] + total[key], 0};
         v.adp_group[key] = g;
       }
     }
@@ -183,21 +201,22 @@ __global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __r
   for (int b = 0; b < groups; b += MP_THREADS) {
     const int g = b + threadIdx.x;
     int t0 = 0;
+    PlanGroup pg{};
     int2 c = make_int2(0, 0);
     if (g < groups) {
-      t0 = v.grp_start[g] / MP_SLOT_ROWS;
-      c.x = (v.grp_end[g] - 1) / MP_SLOT_ROWS - t0 + 1;
-      c.y = (v.grp_end[g] - v.grp_start[g] + MP_TILE - 1) / MP_TILE;
+      pg = v.groups[g];
+      t0 = pg.start / MP_SLOT_ROWS;
+      c.x = (pg.end - 1) / MP_SLOT_ROWS - t0 + 1;
+      c.y = (pg.end - pg.start + MP_TILE - 1) / MP_TILE;
     }
     int2 sum;
     const int2 at = block_scan(c, sh, sum);
     if (g < groups) {
-      v.grp_slot0[g] = carry.x + at.x;
-      v.grp_tile0[g] = carry.y + at.y;
-      for (int k = 0; k < c.x; ++k) {
-        v.slot_group[carry.x + at.x + k] = g;
-        v.slot_tile[carry.x + at.x + k] = t0 + k;
-      }
+      const int s0 = carry.x + at.x, y0 = carry.y + at.y;
+      v.groups[g].slot0 = s0;
+      for (int k = 0; k < c.x; ++k) v.slots[s0 + k] = {pg.adapter, pg.start, pg.end, t0 + k};
+      for (int k = 0; k < c.y; ++k)
+        v.tiles[y0 + k] = {pg.adapter, pg.start + MP_TILE * k, min(MP_TILE, pg.end - pg.start - MP_TILE * k), g};
     }
     carry.x += sum.x, carry.y += sum.y;
   }
@@ -207,23 +226,21 @@ __global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __r
     int lo = 0, hi = carry.x;  // the first slot whose tile is t or later
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (v.slot_tile[mid] < t)
+      if (v.slots[mid].tile < t)
         lo = mid + 1;
       else
         hi = mid;
     }
     v.tile_slot0[t] = lo;
   }
-  if (threadIdx.x == 0) {
-    v.grp_slot0[groups] = carry.x;
-    v.grp_tile0[groups] = carry.y;
-    *v.head = {groups, moved ? 0 : 1, carry.x, carry.y};
-  }
+  if (threadIdx.x == 0) *v.head = {groups, moved ? 0 : 1, carry.x, carry.y};
 }
 
 // Rows of X in sorted order, for batches that are not in it already.
 __global__ void __launch_bounds__(256) multi_sort_rows_kernel(const uint4* __restrict__ X, uint4* __restrict__ Xs,
                                                               int vecs, const PlanView v) {
+  pdl_launch_dependents();
+  pdl_wait();
   if (v.head->in_order) return;
   const int64_t all = static_cast<int64_t>(v.M) * vecs;
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < all;
@@ -239,13 +256,22 @@ __global__ void __launch_bounds__(256) multi_sort_rows_kernel(const uint4* __res
 // K: T = X L1 (kKN: the factor is [K][r]) and U = dY L2^T ([r][K]).  Each part
 // stores its own fp32 sums (pack adds them in order).  mma.sync and not
 // tcgen05: its 16-row granularity lets a group of one token cost one fragment
-// row instead of 128, rows are gathered by cp.async wherever they lie, and the
-// product reads its rows once at 2 r operations a value, so it is bound by
-// memory for r up to 64.  4-deep ring, 64 of K a stage; rows of 144 and 2 RP + 16
-// bytes keep ldmatrix free of bank conflicts.
+// row instead of 128, and rows are gathered by cp.async wherever they lie.  The
+// product reads its rows once at 2 r operations a value, so memory bounds it for
+// r up to 64.  4-deep ring, 64 of K a stage; rows of 144 and 2 RP + 16 bytes keep
+// ldmatrix free of bank conflicts.  Tiles of 128 rows (32 a warp) halve the
+// reads of B from shared memory but leave 8 warps an SM: not faster at 4096 x
+// 4096 (16 us both), slower for small groups (333 tokens: 18 us for 11).
+// Ranks above 128 are further blocks (blockIdx.z).
+// The tensor core cuts its running sum to fp32 at every step, so after every
+// MS_CHAIN stages the sums are added to others in registers: without this the
+// cut is what dL1's error against 64 bits consists of (5.8e-6 of dL1's norm at K =
+// 13824, 1.2e-6 with it; an fp32 product's is 1.3e-6).
 constexpr int MS_THREADS = 128;
 constexpr int MS_K = 64;
 constexpr int MS_PITCH = MS_K * 2 + 16;
+constexpr int MS_CHAIN = 4;       // stages
+constexpr int MS_MAX_RP = 128;    // ranks of a block
 template <int RP, bool kKN>
 constexpr int ms_b_pitch() {
   return kKN ? RP * 2 + 16 : MS_PITCH;
@@ -288,85 +314,75 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
 }
 
-// The group of entry `at` of an ascending list of first entries (len = groups).
-__device__ __forceinline__ int plan_find(const int* first, int len, int at) {
-  int lo = 0, hi = len;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= at)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 template <int RP, bool kKN>
 __global__ void __launch_bounds__(MS_THREADS) multi_shrink_kernel(const ShrinkParams p, const PlanView v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kStages = ms_stages<RP>();
   constexpr int kStage = ms_stage_bytes<RP, kKN>();
   constexpr int kBPitch = ms_b_pitch<RP, kKN>();
-  const int tile = blockIdx.x;
-  pdl_launch_dependents();  // a decode kernel that follows may start its weight stream now
+  pdl_launch_dependents();
   if (p.zero != nullptr)
     for (int64_t q = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * MS_THREADS + threadIdx.x;
          q < p.zero_len / 4; q += static_cast<int64_t>(gridDim.x) * gridDim.y * MS_THREADS)
       reinterpret_cast<float4*>(p.zero)[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (tile >= v.head->tiles) return;
-  const int grp = plan_find(v.grp_tile0, v.head->groups, tile);
-  const int row0 = v.grp_start[grp] + MP_TILE * (tile - v.grp_tile0[grp]);
-  const int nrow = min(MP_TILE, v.grp_end[grp] - row0);
-  const uint16_t* B = p.B + static_cast<int64_t>(v.grp_adapter[grp]) * p.b_stride;
+  const int n_tiles = __ldg(&v.head->tiles);
+  const PlanTile tile = plan_load(v.tiles + blockIdx.x);  // allocated for every block; garbage past n_tiles
+  if (static_cast<int>(blockIdx.x) >= n_tiles) {
+    pdl_wait();
+    return;
+  }
+  const int j0 = static_cast<int>(blockIdx.z) * MS_MAX_RP;
+  const int ranks = min(RP, p.r - j0);
+  const uint16_t* B = p.B + static_cast<int64_t>(tile.adapter) * p.b_stride + (kKN ? j0 : j0 * p.ldb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k0 = blockIdx.y * p.k_per_split;
   const int k1 = min(p.K, k0 + p.k_per_split);
   const int steps = (k1 - k0) / MS_K;
   const uint32_t base = smem_u32(smem_raw);
   // this thread's rows of the A tile: 16 i + tid / 8, 16-byte column tid % 8
+  const int mine = threadIdx.x >> 3;
   const uint16_t* arow[4];
-  bool aok[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int rr = 16 * i + (threadIdx.x >> 3);
-    aok[i] = rr < nrow;
-    arow[i] = p.A + static_cast<int64_t>(v.perm[row0 + (aok[i] ? rr : 0)]) * p.K + 8 * (threadIdx.x & 7);
+    const int rr = 16 * i + mine;
+    arow[i] = p.A + static_cast<int64_t>(__ldg(v.perm + tile.row0 + (rr < tile.rows ? rr : 0))) * p.K + 8 * (threadIdx.x & 7);
   }
   auto load = [&](int s) {
     if (s < steps) {
       const uint32_t st = base + (s % kStages) * kStage;
       const int k = k0 + s * MS_K;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        cp_async16(st + (16 * i + (threadIdx.x >> 3)) * MS_PITCH + 16 * (threadIdx.x & 7), arow[i] + k, aok[i]);
       const uint32_t sb = st + MP_TILE * MS_PITCH;
       if constexpr (kKN) {
         constexpr int kVec = RP / 8;
 #pragma unroll
         for (int q = threadIdx.x; q < MS_K * kVec; q += MS_THREADS) {
           const int kk = q / kVec, c = q % kVec;
-          const bool ok = 8 * c < p.r;
+          const bool ok = 8 * c < ranks;
           cp_async16(sb + kk * kBPitch + 16 * c, B + static_cast<int64_t>(k + kk) * p.ldb + (ok ? 8 * c : 0), ok);
         }
       } else {
 #pragma unroll
         for (int q = threadIdx.x; q < RP * 8; q += MS_THREADS) {
           const int j = q >> 3, c = q & 7;
-          const bool ok = j < p.r;
+          const bool ok = j < ranks;
           cp_async16(sb + j * kBPitch + 16 * c, B + static_cast<int64_t>(ok ? j : 0) * p.ldb + k + 8 * c, ok);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // rows past the group's end are not read: their sums are not stored
+        if (16 * i + mine < tile.rows)
+          cp_async16(st + (16 * i + mine) * MS_PITCH + 16 * (threadIdx.x & 7), arow[i] + k, true);
     }
     cp_async_commit();
   };
-  float acc[RP / 8][4];
+  float acc[RP / 8][4], sum[RP / 8][4];
 #pragma unroll
   for (int j = 0; j < RP / 8; ++j)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[j][c] = 0.0f;
+    for (int c = 0; c < 4; ++c) acc[j][c] = sum[j][c] = 0.0f;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load(s);
-  const bool live = 16 * warp < nrow;
+  const bool live = 16 * warp < tile.rows;
   for (int s = 0; s < steps; ++s) {
     cp_async_wait<kStages - 2>();
     __syncthreads();  // stage s has landed for all, and stage s - 1 has been read by all
@@ -389,18 +405,28 @@ __global__ void __launch_bounds__(MS_THREADS) multi_shrink_kernel(const ShrinkPa
         mma_16816_bf16(acc[2 * j + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
       }
     }
+    if ((s + 1) % MS_CHAIN == 0 || s + 1 == steps) {
+#pragma unroll
+      for (int j = 0; j < RP / 8; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          sum[j][c] += acc[j][c];
+          acc[j][c] = 0.0f;
+        }
+    }
   }
   cp_async_wait<0>();
+  pdl_wait();  // what ran before may still read the parts of an earlier product
   if (!live) return;
-  float* out = p.P + static_cast<int64_t>(blockIdx.y) * v.M * p.r;
+  float* out = p.P + static_cast<int64_t>(blockIdx.y) * v.M * p.r + j0;
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     const int rr = 16 * warp + 8 * hh + (lane >> 2);
-    if (rr >= nrow) continue;
-    float* o = out + static_cast<int64_t>(row0 + rr) * p.r + 2 * (lane & 3);
+    if (rr >= tile.rows) continue;
+    float* o = out + static_cast<int64_t>(tile.row0 + rr) * p.r + 2 * (lane & 3);
 #pragma unroll
     for (int j = 0; j < RP / 8; ++j)
-      if (8 * j < p.r) *reinterpret_cast<float2*>(o + 8 * j) = make_float2(acc[j][2 * hh], acc[j][2 * hh + 1]);
+      if (8 * j < ranks) *reinterpret_cast<float2*>(o + 8 * j) = make_float2(sum[j][2 * hh], sum[j][2 * hh + 1]);
   }
 }
 
@@ -428,7 +454,9 @@ struct PackParams {
 __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, const PlanView v) {
   const PackJob job = blockIdx.z == 0 ? p.job[0] : p.job[1];
   const int slot = blockIdx.x;
+  pdl_launch_dependents();
   if (slot >= p.max_slots) {
+    pdl_wait();
     if (!job.T) return;
     const int row0 = (slot - p.max_slots) * MP_SLOT_ROWS + 64 * blockIdx.y;
     const int vec = p.r / 4;
@@ -439,24 +467,28 @@ __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, con
     }
     return;
   }
-  if (slot >= v.head->slots) return;
-  const int grp = v.slot_group[slot];
-  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp];
-  const float s = p.s[v.grp_adapter[grp]];
-  const int row0 = v.slot_tile[slot] * MP_SLOT_ROWS;
+  const PlanSlot ps = plan_load(v.slots + slot);  // garbage past head->slots
+  if (slot >= __ldg(&v.head->slots)) {
+    pdl_wait();
+    return;
+  }
+  const int g0 = ps.start, g1 = ps.end;
+  const float s = __ldg(p.s + ps.adapter);
+  const int row0 = ps.tile * MP_SLOT_ROWS;
   const int vec = p.rp / 4;
+  pdl_wait();  // the parts of the product
   const int64_t part = static_cast<int64_t>(v.M) * p.r;
   for (int q = threadIdx.x; q < 64 * vec; q += blockDim.x) {
     const int rr = 64 * blockIdx.y + q / vec, c = 4 * (q % vec);
     const int at = row0 + rr;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (at >= g0 && at < g1 && c < p.r) {
-      const int64_t orig = v.perm[at];
+      const int64_t orig = __ldg(v.perm + at);
       if (job.P) {
         const float* src = job.P + static_cast<int64_t>(at) * p.r + c;
 #pragma unroll 4
         for (int k = 0; k < job.splits; ++k) {
-          const float4 f = __ldg(reinterpret_cast<const float4*>(src + k * part));
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src + k * part));
           x[0] += f.x, x[1] += f.y, x[2] += f.z, x[3] += f.w;
         }
       } else {
@@ -532,9 +564,12 @@ __global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const Expan
     }
     return;
   }
-  if (static_cast<int>(blockIdx.y) >= v.head->groups) return;
-  const int grp = blockIdx.y;
-  const int a = v.grp_adapter[grp], g0 = v.grp_start[grp], g1 = v.grp_end[grp];
+  const PlanGroup pg = plan_load(v.groups + blockIdx.y);  // garbage past head->groups
+  if (static_cast<int>(blockIdx.y) >= __ldg(&v.head->groups)) {
+    pdl_wait();
+    return;
+  }
+  const int a = pg.adapter, g0 = pg.start, g1 = pg.end;
   const float s = p.s[a];
   const int vec = tid & 15, slice = tid >> 4;
   const bool in = 8 * vec < cols;
@@ -657,10 +692,10 @@ __device__ __noinline__ float multi_element(const MultiPairParams& p, const Plan
              bf16_bits_to_float(p.Wd[kBwd ? static_cast<int64_t>(k) * p.g.N + n : static_cast<int64_t>(n) * p.K + k]), x);
   const int t = m / MP_SLOT_ROWS;
   for (int s = v.tile_slot0[t]; s < v.tile_slot0[t + 1]; ++s) {
-    const int g = v.slot_group[s];
-    if (m < v.grp_start[g] || m >= v.grp_end[g]) continue;
+    const PlanSlot ps = plan_load(v.slots + s);
+    if (m < ps.start || m >= ps.end) continue;
     const uint16_t* row = p.slots + (static_cast<int64_t>(s) * MP_SLOT_ROWS + m % MP_SLOT_ROWS) * (p.parts * p.rp);
-    const uint16_t* b = p.bank + static_cast<int64_t>(v.grp_adapter[g]) * p.r * p.g.N;
+    const uint16_t* b = p.bank + static_cast<int64_t>(ps.adapter) * p.r * p.g.N;
     float d = 0.0f;
     for (int j = 0; j < p.r; ++j) {
       const float w = bf16_bits_to_float(b[kBwd ? static_cast<int64_t>(n) * p.r + j : static_cast<int64_t>(j) * p.g.N + n]);
@@ -675,8 +710,8 @@ __device__ __noinline__ float multi_element(const MultiPairParams& p, const Plan
 __device__ __forceinline__ bool tile_shared(const MultiPairParams& p, const PlanView& v, int mt) {
   const int s0 = v.tile_slot0[mt], ns = v.tile_slot0[mt + 1] - s0;
   if (ns != 1) return ns > 1;
-  const int g = v.slot_group[s0];
-  return v.grp_start[g] > mt * PG_BM || v.grp_end[g] < min((mt + 1) * PG_BM, p.g.M);
+  const PlanSlot ps = plan_load(v.slots + s0);
+  return ps.start > mt * PG_BM || ps.end < min((mt + 1) * PG_BM, p.g.M);
 }
 
 // Replaces what is not finite among the elements n .. n + kN - 1 of sorted row m by its own sum.
@@ -856,6 +891,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   cluster_barrier();  // both CTAs' barriers initialised and TMEM allocated
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();  // the slots, W' and the sorted rows
   const int nk = mp.even ? *n_even : (pair < n_items ? (n_items - 1 - pair) / npairs + 1 : 0);  // items of this pair
 
   if (warp == 0) {
@@ -893,7 +930,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
             const int e = (i - KM) / mp.chunks;
             const int x = ((i - KM) - e * mp.chunks) * 64;
             const int slot = it.slot0 + e;
-            const int a = v.grp_adapter[v.slot_group[slot]];
+            const int a = __ldg(&v.slots[slot].adapter);
             const int y = slot * MP_SLOT_ROWS + static_cast<int>(rank) * 128;
             tma_load_2d_pair(a_dst, &tmAe, fb, x, y);
             tma_load_2d_pair(a_dst + PG_ATOM_BYTES, &tmAe, fb, mp.rp + x, y);
@@ -1064,7 +1101,11 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
   int mt, n0;
   PairTiles{p.units / p.n_tiles, p.n_tiles}.at(u, mt, n0);
   const int m0 = mt * PG_BM + MR_ROWS * static_cast<int>(blockIdx.y);
-  if (m0 >= p.M) return;
+  pdl_launch_dependents();
+  if (m0 >= p.M) {
+    pdl_wait();
+    return;
+  }
   if (threadIdx.x < 32) {
     const int64_t total = walk_tiles(mp, v, [&](int t, int64_t first, int n) {
       if (t == u) at = first, len = n;
@@ -1078,6 +1119,7 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
   while (c0 > 0 && stage_share(all, c0, pairs).lo > at) --c0;
   int c1 = c0;
   while (stage_share(all, c1, pairs).hi < at + len) ++c1;
+  pdl_wait();
   if (c0 == c1) return;  // one pair computed the whole tile and has stored it
   const int64_t place0 = 2 * c0 + (at > stage_share(all, c0, pairs).lo ? 1 : 0);
   const bool shared = tile_shared(mp, v, mt);
@@ -1107,11 +1149,12 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
 // dL1[a] = X_a^T (s U_a) and dL2[a]^T = dY_a^T (s T_a) over the rows of group a:
 // D is 128 rows of h (or o) by 64 ranks, K runs over the group's 64-row blocks
 // of the sorted order, A from X (or dY) as it lies (M-major), B the slots' three
-// bf16 parts side by side (N-major, N = 192): each part has accumulator columns
-// of its own, added in fp32 at the end, so the rounding of the two small parts'
-// sums does not count and the first part's chain is a third as long (4096 tokens
-// in 4 groups: error against fp64 GRADERR).  The slots are zero in the rows of a
-// block that belong to others.
+// bf16 parts side by side (N-major, N = 192), in other columns of the accumulator
+// from block to block: the first part's sum, whose running value the tensor core
+// cuts to fp32 at every step, is three chains of a third of the length (error of
+// dL2 against 64 bits, 4096 tokens in 4 groups: 2e-6 in one chain, GRADERR in
+// three).  The columns are added in fp32 at the end.  The slots are zero in the
+// rows of a block that belong to others.
 // A group's blocks are dealt to the `split` CTAs of a cluster, whose sums are
 // added in order through distributed shared memory: groups differ in length, a
 // tile's time is its longest group's, and two stages in flight a CTA cover an L2
@@ -1154,7 +1197,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 
 // One element of a factor's gradient from the group's own tokens alone, in fp32.
 __device__ __noinline__ float grad_element(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j) {
-  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp], slot0 = v.grp_slot0[grp];
+  const PlanGroup pg = plan_load(v.groups + grp);
+  const int g0 = pg.start, g1 = pg.end, slot0 = pg.slot0;
   float y = 0.0f;
   for (int row = g0; row < g1; ++row) {
     const int64_t slot_row = static_cast<int64_t>(slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS +
@@ -1195,7 +1239,9 @@ __global__ void __launch_bounds__(MD_THREADS, 2)
   const int rows = min(MD_BM, side.rows - m0), ranks = min(MD_BN, p.r - j0);
   // this CTA's share of the tile's rows of D
   const int r0 = MD_BM * part / kSplit, r1 = min(rows, MD_BM * (part + 1) / kSplit);
+  pdl_launch_dependents();
   if (grp < 0) {  // the same for the whole cluster
+    pdl_wait();
     if (second) {
       for (int q = threadIdx.x; q < (r1 - r0) * ranks; q += MD_THREADS)
         out[static_cast<int64_t>(j0 + q / (r1 - r0)) * side.rows + m0 + r0 + q % (r1 - r0)] = 0.0f;
@@ -1205,12 +1251,13 @@ __global__ void __launch_bounds__(MD_THREADS, 2)
     }
     return;
   }
-  const int g0 = v.grp_start[grp], g1 = v.grp_end[grp];
+  const PlanGroup pg = plan_load(v.groups + grp);
+  const int g0 = pg.start, g1 = pg.end;
   const int blk0 = g0 / MD_BK;
   const int blocks = (g1 - 1) / MD_BK - blk0 + 1;
   const int i0 = blocks * part / kSplit;
   const int S = blocks * (part + 1) / kSplit - i0;
-  const int slot0 = v.grp_slot0[grp];
+  const int slot0 = pg.slot0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MD_STAGES; ++s) {
@@ -1228,6 +1275,7 @@ __global__ void __launch_bounds__(MD_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
 
   if (warp == 0 && lane == 0) {
     const CUtensorMap* ma = second ? (v.head->in_order ? &tmD : &tmDs) : (v.head->in_order ? &tmX : &tmXs);
@@ -1243,7 +1291,8 @@ __global__ void __launch_bounds__(MD_THREADS, 2)
       mbar_arrive_expect_tx(&full[s], MD_STAGE_BYTES);
       tma_load_2d(st, ma, &full[s], m0, row);
       tma_load_2d(st + MD_A_BYTES / 2, ma, &full[s], m0 + 64, row);
-      for (int h = 0; h < MD_PARTS; ++h) tma_load_2d(st + MD_A_BYTES + h * MD_B_BYTES, mb, &full[s], h * p.rp + j0, y);
+      for (int h = 0; h < MD_PARTS; ++h)  // the parts change columns from block to block
+        tma_load_2d(st + MD_A_BYTES + ((h + i) % MD_PARTS) * MD_B_BYTES, mb, &full[s], h * p.rp + j0, y);
       issued = i + 1;
     }
     for (int i = issued - MD_STAGES > 0 ? issued - MD_STAGES : 0; i < issued; ++i)

@@ -1467,6 +1467,9 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Slots of a batch: a 256-row tile has one, and one more for every group that begins inside it.
 int64_t max_slots(int64_t M, int n) { return div_up(M, MP_SLOT_ROWS) + (n < M ? n : M); }
 
+// 64-row tiles of the groups: every group may end in one of its own.
+int64_t max_tiles(int64_t M, int n) { return div_up(M, MP_TILE) + (n < M ? n : M); }
+
 size_t plan_layout(void* base, int64_t M, int n, PlanView* v) {
   uint8_t* p = static_cast<uint8_t*>(base);
   size_t off = 0;
@@ -1475,20 +1478,16 @@ size_t plan_layout(void* base, int64_t M, int n, PlanView* v) {
     off += round256(static_cast<size_t>(ints) * 4);
     return q;
   };
-  const int64_t g = n < M ? n : M, slots = max_slots(M, n), keys = static_cast<int64_t>(n) + 1;
+  const int64_t g = n < M ? n : M, keys = static_cast<int64_t>(n) + 1;
   PlanView w{};
-  w.head = reinterpret_cast<PlanHead*>(take(4));
+  w.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead) / 4));
   w.perm = take(M);
   w.owner = take(M);
-  w.grp_adapter = take(g);
-  w.grp_start = take(g);
-  w.grp_end = take(g);
-  w.grp_slot0 = take(g + 1);
-  w.grp_tile0 = take(g + 1);
+  w.groups = reinterpret_cast<PlanGroup*>(take(4 * (g + 1)));
   w.adp_group = take(n);
-  w.slot_group = take(slots);
-  w.slot_tile = take(slots);
+  w.slots = reinterpret_cast<PlanSlot*>(take(4 * max_slots(M, n)));
   w.tile_slot0 = take(div_up(M, MP_SLOT_ROWS) + 1);
+  w.tiles = reinterpret_cast<PlanTile*>(take(4 * max_tiles(M, n)));
   w.counts = take((MP_WARPS + 3) * keys);
   w.M = static_cast<int>(M);
   w.n = n;
@@ -1565,31 +1564,49 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   return w;
 }
 
+// A kernel as the programmatic dependent of the one before it on the stream.
+template <typename K, typename... Args>
+int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 int sort_rows(const void* X, uint16_t* Xs, int64_t width, const PlanView& v, cudaStream_t st) {
   LaunchScope ls(QLORA_KERNEL_AUX, st);
   const int vecs = static_cast<int>(width / 8);
-  multi_sort_rows_kernel<<<static_cast<unsigned>(grid_for(static_cast<int64_t>(v.M) * vecs, 1024, sm_count() * 8)), 256,
-                           0, st>>>(static_cast<const uint4*>(X), reinterpret_cast<uint4*>(Xs), vecs, v);
-  return launch_status();
+  const dim3 grid(static_cast<unsigned>(grid_for(static_cast<int64_t>(v.M) * vecs, 1024, sm_count() * 8)));
+  return launch_dependent(multi_sort_rows_kernel, grid, 256, 0, st, static_cast<const uint4*>(X),
+                          reinterpret_cast<uint4*>(Xs), vecs, v);
 }
 
 template <int RP, bool kKN>
-int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, cudaStream_t st) {
-  const int smem = ms_stages<RP>() * ms_stage_bytes<RP, kKN>();
+int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, bool first, cudaStream_t st) {
+  constexpr int smem = ms_stages<RP>() * ms_stage_bytes<RP, kKN>();
   if (set_smem(multi_shrink_kernel<RP, kKN>, smem) != QLORA_OK) return QLORA_ERR_CUDA;
-  const int64_t tiles = div_up(v.M, MP_TILE) + (v.n < v.M ? v.n : v.M);
-  {
-    LaunchScope ls(QLORA_KERNEL_TGEMM, st);
-    multi_shrink_kernel<RP, kKN><<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(splits)), MS_THREADS, smem,
-                                   st>>>(p, v);
-  }
+  const dim3 grid(static_cast<unsigned>(max_tiles(v.M, v.n)), static_cast<unsigned>(splits),
+                  static_cast<unsigned>(div_up(p.r, MS_MAX_RP)));
+  LaunchScope ls(QLORA_KERNEL_TGEMM, st);
+  if (!first) return launch_dependent(multi_shrink_kernel<RP, kKN>, grid, MS_THREADS, smem, st, p, v);
+  multi_shrink_kernel<RP, kKN><<<grid, MS_THREADS, smem, st>>>(p, v);
   return launch_status();
 }
 
 // Parts of A B[a] of every group: A [M][K]; kKN: B [n][K][r], else [n][r][K].
+// first: the call's first kernel, launched behind all that came before it; the
+// kernels that follow are programmatic dependents, which set up and read the plan
+// while the one before them ends, and wait for it before they read its results.
 template <bool kKN>
-int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, cudaStream_t st,
-                  float* zero = nullptr, int64_t zero_len = 0) {
+int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, bool first,
+                  cudaStream_t st, float* zero = nullptr, int64_t zero_len = 0) {
   const int splits = shrink_splits(v.M, v.n, K);
   ShrinkParams p{};
   p.A = static_cast<const uint16_t*>(A);
@@ -1602,11 +1619,10 @@ int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, cons
   p.P = P;
   p.zero = zero;
   p.zero_len = zero_len;
-  if (r <= 16) return launch_shrink_as<16, kKN>(p, splits, v, st);
-  if (r <= 32) return launch_shrink_as<32, kKN>(p, splits, v, st);
-  if (r <= 64) return launch_shrink_as<64, kKN>(p, splits, v, st);
-  if (r <= 128) return launch_shrink_as<128, kKN>(p, splits, v, st);
-  return launch_shrink_as<256, kKN>(p, splits, v, st);
+  if (r <= 16) return launch_shrink_as<16, kKN>(p, splits, v, first, st);
+  if (r <= 32) return launch_shrink_as<32, kKN>(p, splits, v, first, st);
+  if (r <= 64) return launch_shrink_as<64, kKN>(p, splits, v, first, st);
+  return launch_shrink_as<128, kKN>(p, splits, v, first, st);
 }
 
 int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int parts, const PlanView& v,
@@ -1620,11 +1636,9 @@ int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int
   p.parts = parts;
   p.max_slots = static_cast<int>(max_slots(v.M, v.n));
   const int64_t x = p.max_slots + div_up(v.M, MP_SLOT_ROWS);
-  {
-    LaunchScope ls(QLORA_KERNEL_AUX, st);
-    multi_pack_kernel<<<dim3(static_cast<unsigned>(x), MP_SLOT_ROWS / 64, j1 ? 2 : 1), 256, 0, st>>>(p, v);
-  }
-  return launch_status();
+  LaunchScope ls(QLORA_KERNEL_AUX, st);
+  return launch_dependent(multi_pack_kernel, dim3(static_cast<unsigned>(x), MP_SLOT_ROWS / 64, j1 ? 2 : 1), 256, 0, st,
+                          p, v);
 }
 
 template <bool kBwd>
@@ -1698,31 +1712,18 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   const int clusters = !p.even || most >= pairs ? pairs : static_cast<int>(most > 1 ? most : 1);
   {
     LaunchScope ls(kBwd ? QLORA_KERNEL_FUSED_BWD : QLORA_KERNEL_FUSED_FWD, st);
-    multi_pair_kernel<kBwd><<<2 * clusters, PG_THREADS, MG_PAIR_SMEM, st>>>(ma, mas, mb, mae, mbe, p, v);
+    if (launch_dependent(multi_pair_kernel<kBwd>, dim3(static_cast<unsigned>(2 * clusters)), PG_THREADS, MG_PAIR_SMEM, st,
+                         ma, mas, mb, mae, mbe, p, v) != QLORA_OK)
+      return QLORA_ERR_CUDA;
   }
   if (p.even && clusters > 1) {
     const int64_t rows = M < PG_BM ? M : PG_BM;
     LaunchScope ls(QLORA_KERNEL_AUX, st);
-    multi_reduce_kernel<kBwd><<<dim3(static_cast<unsigned>(p.g.units), static_cast<unsigned>(div_up(rows, MR_ROWS))),
-                                256, 0, st>>>(p, clusters, v);
+    return launch_dependent(multi_reduce_kernel<kBwd>,
+                            dim3(static_cast<unsigned>(p.g.units), static_cast<unsigned>(div_up(rows, MR_ROWS))), 256, 0,
+                            st, p, clusters, v);
   }
-  return launch_status();
-}
-
-// A kernel as the programmatic dependent of the one before it on the stream.
-template <typename K, typename... Args>
-int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return QLORA_OK;
 }
 
 // The decode forward, three launches: the split-K product T = X L1 of the
@@ -1733,7 +1734,7 @@ int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapte
   const int64_t M = v.M, o = Wq->o, h = Wq->h;
   const int r = ad->r;
   float* acc = y_dtype == QLORA_DTYPE_F32 ? static_cast<float*>(Y) : w.Yacc;
-  int rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st, acc, M * o);
+  int rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, true, st, acc, M * o);
   if (rc != QLORA_OK) return rc;
   CUtensorMap mc, mx;
   if (M <= kDecodeMMax) {
@@ -1833,13 +1834,15 @@ int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlo
     cfg.blockDim = dim3(MD_THREADS);
     cfg.dynamicSmemBytes = MD_SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     LaunchScope ls(QLORA_KERNEL_TGEMM, st);
     return cudaLaunchKernelEx(&cfg, kernel, mx, mxs, md, mds, mu, mt, p, v) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
   };
@@ -1909,8 +1912,9 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
-  if (sort_rows(X, w.Xs, h, v, st) != QLORA_OK) return QLORA_ERR_CUDA;
-  rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st);
+  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
+  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, v, st);
+  if (rc == QLORA_OK) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
   if (rc != QLORA_OK) return rc;
   PackJob j{};
   j.P = w.PT;
@@ -1918,8 +1922,6 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   j.slots = w.ST;
   j.splits = shrink_splits(M, ad->n, h);
   rc = launch_pack(j, nullptr, ad->s, r, 2, v, st);
-  if (rc != QLORA_OK) return rc;
-  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
   if (rc != QLORA_OK) return rc;
   return launch_multi_pair<false>(X, w.Xs, w.ST, ad, w.Wd, o, h, 2, Y, y_dtype == QLORA_DTYPE_BF16, w, v, st);
 }
@@ -1940,9 +1942,11 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   PlanView v;
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (sort_rows(X, w.Xs, h, v, st) != QLORA_OK || sort_rows(dY, w.Ds, o, v, st) != QLORA_OK) return QLORA_ERR_CUDA;
-  rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, st);
-  if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, st);
+  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
+  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, v, st);
+  if (rc == QLORA_OK) rc = sort_rows(dY, w.Ds, o, v, st);
+  if (rc == QLORA_OK) rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, false, st);
+  if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
   if (rc != QLORA_OK) return rc;
   PackJob ju{}, jt{};
   ju.P = w.PU;
@@ -1953,8 +1957,6 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   jt.slots = w.ST;
   jt.splits = shrink_splits(M, ad->n, h);
   rc = launch_pack(ju, &jt, ad->s, r, MD_PARTS, v, st);
-  if (rc != QLORA_OK) return rc;
-  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
   if (rc != QLORA_OK) return rc;
   rc = launch_multi_pair<true>(dY, w.Ds, w.SU, ad, w.Wd, o, h, MD_PARTS, dX, dx_dtype == QLORA_DTYPE_BF16, w, v, st);
   if (rc != QLORA_OK) return rc;
