@@ -236,17 +236,25 @@ __global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __r
   if (threadIdx.x == 0) *v.head = {groups, moved ? 0 : 1, carry.x, carry.y};
 }
 
-// Rows of X in sorted order, for batches that are not in it already.
-__global__ void __launch_bounds__(256) multi_sort_rows_kernel(const uint4* __restrict__ X, uint4* __restrict__ Xs,
-                                                              int vecs, const PlanView v) {
+// Rows of X (blockIdx.y = 0) and dY in sorted order, for batches that are not in it already.
+struct SortParams {
+  const uint4* src[2];
+  uint4* dst[2];
+  int vecs[2];  // 16-byte vectors of a row
+};
+__global__ void __launch_bounds__(256) multi_sort_rows_kernel(const SortParams p, const PlanView v) {
   pdl_launch_dependents();
   pdl_wait();
   if (v.head->in_order) return;
+  const bool second = blockIdx.y == 1;
+  const uint4* src = second ? p.src[1] : p.src[0];
+  uint4* dst = second ? p.dst[1] : p.dst[0];
+  const int vecs = second ? p.vecs[1] : p.vecs[0];
   const int64_t all = static_cast<int64_t>(v.M) * vecs;
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < all;
        q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t p = q / vecs;
-    Xs[q] = __ldg(X + static_cast<int64_t>(v.perm[p]) * vecs + (q - p * vecs));
+    const int64_t p0 = q / vecs;
+    dst[q] = __ldg(src + static_cast<int64_t>(v.perm[p0]) * vecs + (q - p0 * vecs));
   }
 }
 

@@ -114,9 +114,12 @@ int zero_index(const float* q) {
 }
 
 int sm_count() {
+  static std::atomic<int> cache[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev >= 0 && dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -1564,6 +1567,18 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   return w;
 }
 
+// set_smem with the same bytes at every call of a kernel, done once per device.
+template <auto kKernel>
+int set_smem_once(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return QLORA_OK;
+  if (set_smem(kKernel, bytes) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return QLORA_OK;
+}
+
 // A kernel as the programmatic dependent of the one before it on the stream.
 template <typename K, typename... Args>
 int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
@@ -1580,18 +1595,26 @@ int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-int sort_rows(const void* X, uint16_t* Xs, int64_t width, const PlanView& v, cudaStream_t st) {
+// Sorted copies of X (and dY) for batches that are not in the groups' order.
+int sort_rows(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_t* Ds, int64_t d_width,
+              const PlanView& v, cudaStream_t st) {
   LaunchScope ls(QLORA_KERNEL_AUX, st);
-  const int vecs = static_cast<int>(width / 8);
-  const dim3 grid(static_cast<unsigned>(grid_for(static_cast<int64_t>(v.M) * vecs, 1024, sm_count() * 8)));
-  return launch_dependent(multi_sort_rows_kernel, grid, 256, 0, st, static_cast<const uint4*>(X),
-                          reinterpret_cast<uint4*>(Xs), vecs, v);
+  SortParams p{};
+  p.src[0] = static_cast<const uint4*>(X);
+  p.dst[0] = reinterpret_cast<uint4*>(Xs);
+  p.vecs[0] = static_cast<int>(width / 8);
+  p.src[1] = static_cast<const uint4*>(D);
+  p.dst[1] = reinterpret_cast<uint4*>(Ds);
+  p.vecs[1] = static_cast<int>(d_width / 8);
+  const int64_t most = static_cast<int64_t>(v.M) * (width > d_width ? width : d_width) / 8;
+  const dim3 grid(static_cast<unsigned>(grid_for(most, 1024, sm_count() * 8)), D ? 2 : 1);
+  return launch_dependent(multi_sort_rows_kernel, grid, 256, 0, st, p, v);
 }
 
 template <int RP, bool kKN>
 int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, bool first, cudaStream_t st) {
   constexpr int smem = ms_stages<RP>() * ms_stage_bytes<RP, kKN>();
-  if (set_smem(multi_shrink_kernel<RP, kKN>, smem) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (set_smem_once<multi_shrink_kernel<RP, kKN>>(smem) != QLORA_OK) return QLORA_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>(max_tiles(v.M, v.n)), static_cast<unsigned>(splits),
                   static_cast<unsigned>(div_up(p.r, MS_MAX_RP)));
   LaunchScope ls(QLORA_KERNEL_TGEMM, st);
@@ -1671,7 +1694,7 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   if (kBwd ? !map_bf16_3d(&mbe, ad->L1, r, h, ad->n, r * 2, h * r * 2, 64, 128, 1)
            : !map_bf16_3d(&mbe, ad->L2, o, r, ad->n, o * 2, r * o * 2, 64, 64, 1))
     return QLORA_ERR_CUDA;
-  if (set_smem(multi_pair_kernel<kBwd>, MG_PAIR_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (set_smem_once<multi_pair_kernel<kBwd>>(MG_PAIR_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
   int pairs = multi_resident_pairs<kBwd>();
   if (pairs <= 0) return QLORA_ERR_CUDA;
   if (pairs > (sm_count() + 1) / 2) pairs = (sm_count() + 1) / 2;  // the partial buffer's bound
@@ -1913,7 +1936,7 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
   rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
-  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, v, st);
+  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, nullptr, nullptr, 0, v, st);
   if (rc == QLORA_OK) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
   if (rc != QLORA_OK) return rc;
   PackJob j{};
@@ -1943,8 +1966,7 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
-  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, v, st);
-  if (rc == QLORA_OK) rc = sort_rows(dY, w.Ds, o, v, st);
+  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, dY, w.Ds, o, v, st);
   if (rc == QLORA_OK) rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, false, st);
   if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
   if (rc != QLORA_OK) return rc;
