@@ -524,19 +524,23 @@ __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, con
 
 // The adapter term of a batch of up to 32 tokens, added to the finished base
 // product: Y[i] = acc[i] + s[a] sum_j T[i][j] L2[a][j] for one group
-// (blockIdx.y) and 128 columns (blockIdx.x); blockIdx.y = max_groups: the tokens
-// without adapter.  L2 is the only large operand (2 r o bytes an adapter), read
-// once for up to four tokens: 16 threads of 8 columns each by 16 slices of the
-// ranks, four rows a thread in flight.  The first rows are loaded before the
-// wait for the base product.  T is summed from its parts in order, the slices
-// through shared memory in order.  A pass of its own and not a share of the
-// decode kernel's warps: three warps an SM cannot keep enough loads in flight
-// beside a ring that fills the shared memory (16 adapters of rank 64, 8192 x
-// 22016: 114 to 140 us for the two in one kernel, 68 + EXPAND16 apart).
+// (blockIdx.y) and a share of the columns (blockIdx.x); blockIdx.y = max_groups:
+// the tokens without adapter.  L2 is the only large operand (2 r o bytes an
+// adapter), read once for up to two tokens: the block's threads are S slices of
+// the ranks by 256 / S column vectors of 8, eight rows a thread in flight, the
+// first of them loaded before the wait for the base product; the slices are added
+// through shared memory in order.  Few slices leave few blocks, each with more
+// loads: 16 adapters of rank 64 and 22016 columns take 20 us with 16 slices (2752
+// blocks, whose set-up is most of it) and 12 with 4; a single token of 4096
+// columns needs the 16 to have 32 blocks at all.
+// A kernel of its own and not a share of the decode kernel's warps: three warps an
+// SM cannot keep enough loads in flight beside a ring that fills the shared memory
+// (the same 16 adapters: 114 to 140 us for the two in one kernel, 59 for the
+// weight stream alone).
 constexpr int MX_THREADS = 256;
-constexpr int MX_COLS = 128;
-constexpr int MX_SLICES = 16;
-constexpr int MX_MT = 4;
+constexpr int MX_MT = 2;
+constexpr int MX_ROWS = 8;
+constexpr int mx_cols(int slices) { return MX_THREADS / slices * 8; }
 
 struct ExpandParams {
   const float* P;      // [parts][M][r] of T, sorted rows
@@ -548,27 +552,25 @@ struct ExpandParams {
   int parts, r, N, max_groups;
 };
 
-template <bool kBf16>
-__global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const ExpandParams p, const PlanView v) {
+template <bool kBf16, int S>
+__global__ void __launch_bounds__(MX_THREADS, 3) multi_expand_kernel(const ExpandParams p, const PlanView v) {
+  constexpr int kVecs = MX_THREADS / S, kCols = mx_cols(S);
   __shared__ __align__(16) float Ts[MX_MT * QLORA_MAX_RANK];
-  __shared__ __align__(16) float red[MX_SLICES * MX_MT * MX_COLS];
+  __shared__ __align__(16) float red[MX_MT * MX_THREADS * 8];  // [token][slice][column]
   const int tid = threadIdx.x;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * MX_COLS;
-  const int cols = static_cast<int>(p.N - n0 < MX_COLS ? p.N - n0 : MX_COLS);  // a multiple of 64
-  auto put = [&](int64_t m, int64_t n, float y) {
-    if constexpr (kBf16)
-      static_cast<uint16_t*>(p.Y)[m * p.N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-    else
-      static_cast<float*>(p.Y)[m * p.N + n] = y;
-  };
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCols;
+  const int cols = static_cast<int>(p.N - n0 < kCols ? p.N - n0 : kCols);  // a multiple of 64
   if (static_cast<int>(blockIdx.y) == p.max_groups) {
     pdl_wait();
     for (int m = 0; m < v.M; ++m) {
       if (v.owner[m] >= 0) continue;
       if (p.T && blockIdx.x == 0)
         for (int j = tid; j < p.r; j += MX_THREADS) p.T[static_cast<int64_t>(m) * p.r + j] = 0.0f;
-      if (kBf16)
-        for (int c = tid; c < cols; c += MX_THREADS) put(m, n0 + c, p.acc[static_cast<int64_t>(m) * p.N + n0 + c]);
+      if constexpr (kBf16)
+        for (int c = tid; c < cols; c += MX_THREADS) {
+          const int64_t at = static_cast<int64_t>(m) * p.N + n0 + c;
+          static_cast<uint16_t*>(p.Y)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(p.acc[at]));
+        }
     }
     return;
   }
@@ -578,26 +580,26 @@ __global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const Expan
     return;
   }
   const int a = pg.adapter, g0 = pg.start, g1 = pg.end;
-  const float s = p.s[a];
-  const int vec = tid & 15, slice = tid >> 4;
+  const float s = __ldg(p.s + a);
+  const int vec = tid % kVecs, slice = tid / kVecs;
   const bool in = 8 * vec < cols;
   const uint16_t* L2 = p.L2 + static_cast<int64_t>(a) * p.r * p.N + n0 + 8 * vec;
-  auto load = [&](int j0, uint4 (&w)[4]) {
+  auto load = [&](int j0, uint4 (&w)[MX_ROWS]) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = j0 + slice + u * MX_SLICES;
+    for (int u = 0; u < MX_ROWS; ++u) {
+      const int j = j0 + slice + u * S;
       w[u] = in && j < p.r ? __ldg(reinterpret_cast<const uint4*>(L2 + static_cast<int64_t>(j) * p.N))
                            : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  uint4 w[4];
+  uint4 w[MX_ROWS];
   load(0, w);
   pdl_wait();
   for (int m0 = g0; m0 < g1; m0 += MX_MT) {
     const int mt = min(MX_MT, g1 - m0);
     // T of these tokens: groups of threads take every sub-th part, then the groups are added in order
     const int nt4 = mt * p.r / 4;  // float4s, 2 .. 256
-    const int subs = MX_THREADS / nt4;
+    const int subs = min(MX_THREADS / nt4, p.parts);
     const int q = tid % nt4, sub = tid / nt4;
     if (sub < subs) {
       const float4* src = reinterpret_cast<const float4*>(p.P + static_cast<int64_t>(m0) * p.r) + q;
@@ -627,11 +629,11 @@ __global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const Expan
     for (int m = 0; m < MX_MT; ++m)
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[m][c] = 0.0f;
-    for (int j0 = 0; j0 < p.r; j0 += 4 * MX_SLICES) {
+    for (int j0 = 0; j0 < p.r; j0 += MX_ROWS * S) {
       if (j0 > 0 || m0 > g0) load(j0, w);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + slice + u * MX_SLICES;
+      for (int u = 0; u < MX_ROWS; ++u) {
+        const int j = j0 + slice + u * S;
         if (j >= p.r) break;
         const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
@@ -649,19 +651,28 @@ __global__ void __launch_bounds__(MX_THREADS, 4) multi_expand_kernel(const Expan
 #pragma unroll
     for (int m = 0; m < MX_MT; ++m) {
       if (m >= mt) break;
-      float4* d = reinterpret_cast<float4*>(red + (slice * MX_MT + m) * MX_COLS + 8 * vec);
+      float4* d = reinterpret_cast<float4*>(red + (m * S + slice) * kCols + 8 * vec);
       d[0] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       d[1] = make_float4(acc[m][4], acc[m][5], acc[m][6], acc[m][7]);
     }
     __syncthreads();
-    for (int q2 = tid; q2 < mt * MX_COLS; q2 += MX_THREADS) {
-      const int m = q2 / MX_COLS, c = q2 % MX_COLS;
+    for (int e = tid; e < mt * (kCols / 4); e += MX_THREADS) {  // four columns of a token a thread
+      const int m = e / (kCols / 4), c = 4 * (e % (kCols / 4));
       if (c >= cols) continue;
-      float sum = 0.0f;
+      const int64_t at = static_cast<int64_t>(v.perm[m0 + m]) * p.N + n0 + c;
+      const float4 base = *reinterpret_cast<const float4*>(p.acc + at);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < MX_SLICES; ++k) sum += red[(k * MX_MT + m) * MX_COLS + c];
-      const int64_t row = v.perm[m0 + m];
-      put(row, n0 + c, fmaf(s, sum, p.acc[row * p.N + n0 + c]));
+      for (int k = 0; k < S; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(red + (m * S + k) * kCols + c);
+        f.x += x.x, f.y += x.y, f.z += x.z, f.w += x.w;
+      }
+      f = make_float4(fmaf(s, f.x, base.x), fmaf(s, f.y, base.y), fmaf(s, f.z, base.z), fmaf(s, f.w, base.w));
+      if constexpr (kBf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.Y) + at) =
+            make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.Y) + at) = f;
     }
     __syncthreads();
   }
@@ -1157,31 +1168,31 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
 // dL1[a] = X_a^T (s U_a) and dL2[a]^T = dY_a^T (s T_a) over the rows of group a:
 // D is 128 rows of h (or o) by 64 ranks, K runs over the group's 64-row blocks
 // of the sorted order, A from X (or dY) as it lies (M-major), B the slots' three
-// bf16 parts side by side (N-major, N = 192), in other columns of the accumulator
-// from block to block: the first part's sum, whose running value the tensor core
-// cuts to fp32 at every step, is three chains of a third of the length (error of
-// dL2 against 64 bits, 4096 tokens in 4 groups: 2e-6 in one chain, GRADERR in
-// three).  The columns are added in fp32 at the end.  The slots are zero in the
-// rows of a block that belong to others.
-// A group's blocks are dealt to the `split` CTAs of a cluster, whose sums are
-// added in order through distributed shared memory: groups differ in length, a
-// tile's time is its longest group's, and two stages in flight a CTA cover an L2
-// latency only with several CTAs on a group.  No sum depends on timing; adapters
-// without tokens get zeros.  blockIdx.x: the CTAs of each tile of dL1, then of
-// dL2; blockIdx.y: adapter.
+// bf16 parts side by side (N-major, N = 192, each part in accumulator columns of
+// its own).  The slots are zero in the rows of a block that belong to others.
+// Persistent, one CTA an SM: one thread loads (5 stages of 40 KB), one issues the
+// MMAs, four warps add the accumulators to their registers in fp32 after every
+// MD_CHAIN blocks (two accumulators, so that the MMAs go on) and store a finished
+// tile.  The chain is short because the tensor core cuts its running sum to fp32
+// at every step: error of dL2 against 64 bits, 4096 tokens in 4 groups, 2e-6 with
+// a group in one chain, GRADERR so (an fp32 product's is 7e-7).  One CTA for each
+// tile and group took 31 us there and 88 us for 8190 tokens, 5120 x 13824, most of
+// it the start and end of blocks that hold two stages; GRAD4096 and GRAD8190 so.
+// When the tiles are fewer than the SMs a group's blocks are dealt to `split`
+// items, whose sums go to the partial buffer and are added in order by the one
+// that ends last.  No sum depends on timing; adapters without tokens get zeros.
 constexpr int MD_BM = 128;
 constexpr int MD_BN = 64;
 constexpr int MD_BK = 64;
-constexpr int MD_THREADS = 128;
+constexpr int MD_THREADS = 192;
 constexpr int MD_PARTS = 3;
+constexpr int MD_CHAIN = 8;
+constexpr int MD_STAGES = 5;
 constexpr int MD_A_BYTES = MD_BM * MD_BK * 2;
 constexpr int MD_B_BYTES = MD_BN * MD_BK * 2;
 constexpr int MD_STAGE_BYTES = MD_A_BYTES + MD_PARTS * MD_B_BYTES;
-constexpr int MD_STAGES = 2;               // two CTAs an SM
-constexpr int MD_SUM_PITCH = MD_BN + 4;    // floats a row of the CTA's sums (over the ring)
-constexpr int MD_SMEM = MD_STAGES * MD_STAGE_BYTES + 1024 + 128;
-constexpr uint32_t MD_TMEM_COLS = 256;     // 192 used
-static_assert(MD_BM * MD_SUM_PITCH * 4 <= MD_STAGES * MD_STAGE_BYTES, "the sums fit the ring");
+constexpr int MD_SMEM = MD_STAGES * MD_STAGE_BYTES + 1024 + 256;
+constexpr uint32_t MD_TMEM_COLS = 512;  // two accumulators of 192, 256 apart
 
 struct MultiGradSide {
   const uint16_t* A;      // X or dY, batch order
@@ -1192,25 +1203,21 @@ struct MultiGradSide {
 
 struct MultiGradParams {
   MultiGradSide side[2];
-  int r, rp;
-  int tiles0;  // 128-row tiles of dL1, times the rank tiles
+  int r, rp, n;
+  int tiles0;          // 128-row tiles of dL1, times the rank tiles
+  int tiles;           // and of dL2
+  int split;           // parts of a group's blocks
+  float* partial;      // [items][128][64]
+  unsigned* counters;  // [tiles * n], zero at launch
 };
-
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 
 // One element of a factor's gradient from the group's own tokens alone, in fp32.
 __device__ __noinline__ float grad_element(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j) {
   const PlanGroup pg = plan_load(v.groups + grp);
-  const int g0 = pg.start, g1 = pg.end, slot0 = pg.slot0;
   float y = 0.0f;
-  for (int row = g0; row < g1; ++row) {
-    const int64_t slot_row = static_cast<int64_t>(slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS +
-                             row % MP_SLOT_ROWS;
+  for (int row = pg.start; row < pg.end; ++row) {
+    const int64_t slot_row =
+        static_cast<int64_t>(pg.slot0 + row / MP_SLOT_ROWS - pg.start / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
     const uint16_t* b = side.slots + slot_row * (MD_PARTS * rp) + j;
     const float w = bf16_bits_to_float(b[0]) + bf16_bits_to_float(b[rp]) + bf16_bits_to_float(b[2 * rp]);
     y = fmaf(bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]), w, y);
@@ -1218,61 +1225,59 @@ __device__ __noinline__ float grad_element(const MultiGradSide& side, const Plan
   return y;
 }
 
-template <int kSplit>
-__global__ void __launch_bounds__(MD_THREADS, 2)
+__global__ void __launch_bounds__(MD_THREADS, 1)
     multi_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                       const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDs,
                       const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmT,
                       const __grid_constant__ MultiGradParams p, const __grid_constant__ PlanView v) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + MD_STAGES * MD_STAGE_BYTES);
   uint64_t* empty = full + MD_STAGES;
-  uint64_t* accum = empty + MD_STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
-  float* sums = reinterpret_cast<float*>(smem);  // [128][MD_SUM_PITCH], once the ring is done with
+  uint64_t* tfull = empty + MD_STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int index = static_cast<int>(blockIdx.x) / kSplit, part = static_cast<int>(blockIdx.x) % kSplit;
-  const int second = index >= p.tiles0 ? 1 : 0;
-  const MultiGradSide side = second ? p.side[1] : p.side[0];
   const int n_tiles = p.rp / MD_BN;
-  const int tile = index - (second ? p.tiles0 : 0);
-  const int m0 = (tile / n_tiles) * MD_BM;
-  const int j0 = (tile % n_tiles) * MD_BN;
-  const int adapter = blockIdx.y;
-  const int grp = v.adp_group[adapter];
-  float* out = side.out + static_cast<int64_t>(adapter) * p.r * side.rows;
-  const int rows = min(MD_BM, side.rows - m0), ranks = min(MD_BN, p.r - j0);
-  // this CTA's share of the tile's rows of D
-  const int r0 = MD_BM * part / kSplit, r1 = min(rows, MD_BM * (part + 1) / kSplit);
-  pdl_launch_dependents();
-  if (grp < 0) {  // the same for the whole cluster
-    pdl_wait();
-    if (second) {
-      for (int q = threadIdx.x; q < (r1 - r0) * ranks; q += MD_THREADS)
-        out[static_cast<int64_t>(j0 + q / (r1 - r0)) * side.rows + m0 + r0 + q % (r1 - r0)] = 0.0f;
-    } else {
-      for (int q = threadIdx.x; q < (r1 - r0) * ranks; q += MD_THREADS)
-        out[static_cast<int64_t>(m0 + r0 + q / ranks) * p.r + j0 + q % ranks] = 0.0f;
+  const int64_t items = static_cast<int64_t>(p.tiles) * p.n * p.split;
+  // item u: part u % split of tile (u / split) % tiles of an adapter, so that an SM's items
+  // are of different adapters
+  struct Item {
+    int second, m0, j0, adapter, grp;
+    int i0, blocks;  // 64-row blocks i0 .. i0 + blocks - 1 of the sorted order
+    PlanGroup pg;
+  };
+  auto item_of = [&](int64_t u) -> Item {
+    Item it{};
+    const int part = static_cast<int>(u % p.split);
+    const int64_t w = u / p.split;
+    it.adapter = static_cast<int>(w / p.tiles);
+    int tile = static_cast<int>(w - static_cast<int64_t>(it.adapter) * p.tiles);
+    it.second = tile >= p.tiles0 ? 1 : 0;
+    if (it.second) tile -= p.tiles0;
+    it.m0 = (tile / n_tiles) * MD_BM;
+    it.j0 = (tile % n_tiles) * MD_BN;
+    it.grp = __ldg(v.adp_group + it.adapter);
+    if (it.grp >= 0) {
+      it.pg = plan_load(v.groups + it.grp);
+      const int b0 = it.pg.start / MD_BK, b = (it.pg.end - 1) / MD_BK - b0 + 1;
+      it.i0 = b0 + b * part / p.split;
+      it.blocks = b0 + b * (part + 1) / p.split - it.i0;
     }
-    return;
-  }
-  const PlanGroup pg = plan_load(v.groups + grp);
-  const int g0 = pg.start, g1 = pg.end;
-  const int blk0 = g0 / MD_BK;
-  const int blocks = (g1 - 1) / MD_BK - blk0 + 1;
-  const int i0 = blocks * part / kSplit;
-  const int S = blocks * (part + 1) / kSplit - i0;
-  const int slot0 = pg.slot0;
+    return it;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MD_STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(accum, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -1283,112 +1288,163 @@ __global__ void __launch_bounds__(MD_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
   pdl_wait();
 
-  if (warp == 0 && lane == 0) {
-    const CUtensorMap* ma = second ? (v.head->in_order ? &tmD : &tmDs) : (v.head->in_order ? &tmX : &tmXs);
-    const CUtensorMap* mb = second ? &tmT : &tmU;
-    int issued = 0;
-    for (int i = 0; i < S; ++i) {
-      const int s = i % MD_STAGES;
-      if (!mbar_wait(&empty[s], ((i / MD_STAGES) & 1) ^ 1)) break;
-      uint8_t* st = smem + s * MD_STAGE_BYTES;
-      const int row = (blk0 + i0 + i) * MD_BK;
-      // the block's rows within the group's slots
-      const int y = (slot0 + row / MP_SLOT_ROWS - g0 / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
-      mbar_arrive_expect_tx(&full[s], MD_STAGE_BYTES);
-      tma_load_2d(st, ma, &full[s], m0, row);
-      tma_load_2d(st + MD_A_BYTES / 2, ma, &full[s], m0 + 64, row);
-      for (int h = 0; h < MD_PARTS; ++h)  // the parts change columns from block to block
-        tma_load_2d(st + MD_A_BYTES + ((h + i) % MD_PARTS) * MD_B_BYTES, mb, &full[s], h * p.rp + j0, y);
-      issued = i + 1;
-    }
-    for (int i = issued - MD_STAGES > 0 ? issued - MD_STAGES : 0; i < issued; ++i)
-      mbar_wait(&full[i % MD_STAGES], (i / MD_STAGES) & 1);
-  } else if (warp == 1 && lane == 0 && S > 0) {
-    const uint32_t idesc = idesc_bf16(MD_BM, MD_PARTS * MD_BN, true, true);
-    for (int i = 0; i < S; ++i) {
-      const int s = i % MD_STAGES;
-      if (!mbar_wait(&full[s], (i / MD_STAGES) & 1)) break;
-      tc_fence_after();
-      const uint32_t a_base = smem_u32(smem + s * MD_STAGE_BYTES);
-#pragma unroll
-      for (int kk = 0; kk < MD_BK / 16; ++kk)
-        umma_bf16(tmem, sw128_desc(a_base + kk * 2048, MD_A_BYTES / 2, 1024),
-                  sw128_desc(a_base + MD_A_BYTES + kk * 2048, MD_B_BYTES, 1024), idesc, (i > 0 || kk > 0) ? 1u : 0u);
-      umma_commit(&empty[s]);
-    }
-    umma_commit(accum);
-  }
-
-  __syncwarp();
-  const bool ok = S == 0 || mbar_wait(accum, 0);
-  tc_fence_after();
-  __syncthreads();  // the ring is free: every copy has landed (the producer waited) and every MMA is done
-  {
-    float* row = sums + threadIdx.x * MD_SUM_PITCH;
-    for (int c = 0; c < MD_BN; c += 16) {
-      float x[16];
-#pragma unroll
-      for (int t = 0; t < 16; ++t) x[t] = 0.0f;
-      if (S > 0 && ok) {
-        uint32_t a[16], b[16], d[16];
-        const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
-        tmem_ld16(at, a);
-        tmem_ld16(at + MD_BN, b);
-        tmem_ld16(at + 2 * MD_BN, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int t = 0; t < 16; ++t)
-          x[t] = __uint_as_float(a[t]) + (__uint_as_float(b[t]) + __uint_as_float(d[t]));
+  if (warp == 0) {
+    if (lane == 0) {
+      const bool in_order = v.head->in_order != 0;
+      int G = 0;
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < items && ok; u += gridDim.x) {
+        const Item it = item_of(u);
+        const CUtensorMap* ma = it.second ? (in_order ? &tmD : &tmDs) : (in_order ? &tmX : &tmXs);
+        const CUtensorMap* mb = it.second ? &tmT : &tmU;
+        for (int i = 0; i < it.blocks; ++i, ++G) {
+          const int s = G % MD_STAGES;
+          if (!mbar_wait(&empty[s], ((G / MD_STAGES) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * MD_STAGE_BYTES;
+          const int row = (it.i0 + i) * MD_BK;
+          // the block's rows within the group's slots
+          const int y = (it.pg.slot0 + row / MP_SLOT_ROWS - it.pg.start / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
+          mbar_arrive_expect_tx(&full[s], MD_STAGE_BYTES);
+          tma_load_2d(st, ma, &full[s], it.m0, row);
+          tma_load_2d(st + MD_A_BYTES / 2, ma, &full[s], it.m0 + 64, row);
+          for (int h = 0; h < MD_PARTS; ++h)
+            tma_load_2d(st + MD_A_BYTES + h * MD_B_BYTES, mb, &full[s], h * p.rp + it.j0, y);
+        }
       }
+      for (int g = G - MD_STAGES > 0 ? G - MD_STAGES : 0; g < G; ++g) mbar_wait(&full[g % MD_STAGES], (g / MD_STAGES) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(MD_BM, MD_PARTS * MD_BN, true, true);
+      int G = 0, C = 0;  // stages and chains so far
+      bool ok = true;
+      for (int64_t u = blockIdx.x; u < items && ok; u += gridDim.x) {
+        const Item it = item_of(u);
+        for (int c = 0; c < it.blocks && ok; c += MD_CHAIN, ++C) {
+          if (!mbar_wait(&tempty[C & 1], ((C >> 1) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int end = min(it.blocks, c + MD_CHAIN);
+          for (int i = c; i < end; ++i, ++G) {
+            const int s = G % MD_STAGES;
+            if (!mbar_wait(&full[s], (G / MD_STAGES) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(smem + s * MD_STAGE_BYTES);
 #pragma unroll
-      for (int t = 0; t < 16; t += 4)
-        *reinterpret_cast<float4*>(row + c + t) = make_float4(x[t], x[t + 1], x[t + 2], x[t + 3]);
+            for (int kk = 0; kk < MD_BK / 16; ++kk)
+              umma_bf16(tmem + 256u * (C & 1), sw128_desc(a_base + kk * 2048, MD_A_BYTES / 2, 1024),
+                        sw128_desc(a_base + MD_A_BYTES + kk * 2048, MD_B_BYTES, 1024), idesc, (i > c || kk > 0) ? 1u : 0u);
+            umma_commit(&empty[s]);
+          }
+          if (ok) umma_commit(&tfull[C & 1]);
+        }
+      }
+    }
+  } else {
+    // ---------------- epilogue: thread = row of the tile
+    const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
+    const int row = 32 * q + lane;
+    int C = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < items && ok; u += gridDim.x) {
+      const Item it = item_of(u);
+      const MultiGradSide& side = p.side[it.second];
+      float x[MD_BN];
+#pragma unroll
+      for (int j = 0; j < MD_BN; ++j) x[j] = 0.0f;
+      for (int c = 0; c < it.blocks; c += MD_CHAIN, ++C) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[C & 1], (C >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + 256u * (C & 1);
+#pragma unroll
+        for (int h = MD_PARTS - 1; h >= 0; --h)
+#pragma unroll
+          for (int k = 0; k < MD_BN; k += 16) {
+            uint32_t r[16];
+            tmem_ld16(at + h * MD_BN + k, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int t = 0; t < 16; ++t) x[k + t] += __uint_as_float(r[t]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[C & 1]);
+      }
+      if (!ok) break;
+      const int64_t tile_index = u / p.split;
+      if (p.split > 1) {
+        float* part = p.partial + u * (MD_BM * MD_BN) + row;  // [rank][row]: coalesced
+#pragma unroll
+        for (int j = 0; j < MD_BN; ++j) part[j * MD_BM] = x[j];
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue warps
+        __shared__ unsigned order;
+        if (threadIdx.x == 64) order = atomicAdd(&p.counters[tile_index], 1u);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const bool last = order == static_cast<unsigned>(p.split - 1);
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // order has been read by all
+        if (!last) continue;
+        __threadfence();
+        const float* first = p.partial + tile_index * p.split * (MD_BM * MD_BN) + row;
+#pragma unroll
+        for (int j = 0; j < MD_BN; ++j) x[j] = __ldcg(first + j * MD_BM);
+        for (int k = 1; k < p.split; ++k)
+#pragma unroll
+          for (int j = 0; j < MD_BN; ++j) x[j] += __ldcg(first + (k * MD_BN + j) * MD_BM);
+      }
+      const int m = it.m0 + row;
+      if (m >= side.rows) continue;
+      // rows of others in the group's first or last block
+      if (it.grp >= 0 && (it.pg.start % MD_BK != 0 || (it.pg.end % MD_BK != 0 && it.pg.end < v.M))) {
+        float z = 0.0f;
+#pragma unroll
+        for (int j = 0; j < MD_BN; ++j) z = fmaf(x[j], 0.0f, z);
+        if (z != 0.0f)
+          for (int t = 0; t < MD_BN && it.j0 + t < p.r; ++t) {
+            float y = 0.0f;
+#pragma unroll
+            for (int j = 0; j < MD_BN; ++j) y = j == t ? x[j] : y;
+            if (isfinite(y)) continue;
+            y = grad_element(side, v, it.grp, p.rp, m, it.j0 + t);
+#pragma unroll
+            for (int j = 0; j < MD_BN; ++j) x[j] = j == t ? y : x[j];
+          }
+      }
+      float* out = side.out + static_cast<int64_t>(it.adapter) * p.r * side.rows;
+      const int ranks = min(MD_BN, p.r - it.j0);
+      if (it.second) {
+#pragma unroll
+        for (int j = 0; j < MD_BN; ++j)
+          if (j < ranks) out[static_cast<int64_t>(it.j0 + j) * side.rows + m] = x[j];
+      } else {
+        float4* dst = reinterpret_cast<float4*>(out + static_cast<int64_t>(m) * p.r + it.j0);
+#pragma unroll
+        for (int j = 0; j < MD_BN; j += 4)
+          if (j < ranks) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      }
     }
   }
+  __syncwarp();
   tc_fence_before();
-  if (kSplit > 1)
-    cluster_barrier();  // the sums of all CTAs are in shared memory
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, MD_TMEM_COLS);
   }
-  // rows of others in the group's first or last block
-  const bool shared = g0 % MD_BK != 0 || (g1 % MD_BK != 0 && g1 < v.M);
-  // four ranks of a row a thread; for dL2 neighbouring threads take neighbouring rows
-  constexpr int kRows = MD_BM / kSplit;
-  constexpr int kEach = kRows * (MD_BN / 4) / MD_THREADS;  // float4s a thread
-  auto row_of = [&](int q) { return r0 + (second ? q % kRows : q / (MD_BN / 4)); };
-  auto rank_of = [&](int q) { return 4 * (second ? q / kRows : q % (MD_BN / 4)); };
-#pragma unroll 1
-  for (int e = 0; e < kEach; ++e) {
-    const int q = threadIdx.x + e * MD_THREADS;
-    const int m = row_of(q), c = rank_of(q);
-    if (m >= r1 || c >= ranks) continue;
-    float* src = sums + m * MD_SUM_PITCH + c;
-    float4 f[kSplit];  // all loads before the first sum: a remote one takes most of a microsecond
-#pragma unroll
-    for (int k = 0; k < kSplit; ++k)
-      f[k] = kSplit == 1 ? *reinterpret_cast<const float4*>(src) : ld_cluster_v4(cluster_addr(src, static_cast<uint32_t>(k)));
-    float x[4] = {f[0].x, f[0].y, f[0].z, f[0].w};
-#pragma unroll
-    for (int k = 1; k < kSplit; ++k) x[0] += f[k].x, x[1] += f[k].y, x[2] += f[k].z, x[3] += f[k].w;
-    if (shared) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (!isfinite(x[t])) x[t] = grad_element(side, v, grp, p.rp, m0 + m, j0 + c + t);
-    }
-    if (second) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) out[static_cast<int64_t>(j0 + c + t) * side.rows + m0 + m] = x[t];
-    } else {
-      *reinterpret_cast<float4*>(out + static_cast<int64_t>(m0 + m) * p.r + j0 + c) = make_float4(x[0], x[1], x[2], x[3]);
-    }
-  }
-  if (kSplit > 1) cluster_barrier();  // no CTA leaves while another still reads its sums
 }
 
 }  // namespace qlora

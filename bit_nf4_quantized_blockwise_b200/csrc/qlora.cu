@@ -1518,6 +1518,18 @@ int shrink_splits(int64_t M, int n, int64_t K) {
 // Forward calls of up to this many tokens stream the 4-bit weight through the decode kernel.
 constexpr int64_t kMultiDecodeMax = 32;
 
+// Parts of a group's rows in the gradient kernel: as many as give every SM an item, up to eight.
+int grad_split(int64_t M, int n, int64_t tiles) {
+  const int64_t items = tiles * (n < M ? n : M);
+  int split = 1;
+  while (split < 8 && items * split < sm_count() && split * 2 * MD_BK <= M) split *= 2;
+  return split;
+}
+
+int64_t grad_tiles(int64_t o, int64_t h, int r) {
+  return (div_up(h, MD_BM) + div_up(o, MD_BM)) * (rank_pad(r) / MD_BN);
+}
+
 struct MultiWs {
   float* Yacc;     // [M][o] fp32 accumulator of the decode forward (bf16 output)
   float* Tsum;     // [M][r] T of the decode forward, sorted rows
@@ -1530,6 +1542,8 @@ struct MultiWs {
   uint16_t* Wd;    // W'^T
   float* Wpart;
   unsigned* Wcnt;
+  float* Gpart;    // partial sums of the gradients (groups in parts)
+  unsigned* Gcnt;
   size_t bytes;
 };
 
@@ -1563,6 +1577,13 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   const int64_t units = div_up(M, PG_BM) * div_up(bwd ? h : o, PG_BN);
   w.Wpart = static_cast<float*>(take((units < pairs ? 2 : 1) * pairs * PG_BM * PG_BN * 4));
   w.Wcnt = static_cast<unsigned*>(take(pairs * 8 * 4));
+  if (bwd) {
+    const int64_t items = grad_tiles(o, h, r) * n, split = grad_split(M, n, grad_tiles(o, h, r));
+    if (split > 1) {
+      w.Gpart = static_cast<float*>(take(items * split * MD_BM * MD_BN * 4));
+      w.Gcnt = static_cast<unsigned*>(take(items * 4));
+    }
+  }
   w.bytes = off;
   return w;
 }
@@ -1824,10 +1845,15 @@ int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapte
   ep.r = r;
   ep.N = static_cast<int>(o);
   ep.max_groups = static_cast<int>(ad->n < M ? ad->n : M);
-  const dim3 grid(static_cast<unsigned>(div_up(o, MX_COLS)), static_cast<unsigned>(ep.max_groups + 1));
+  // 16 slices of the ranks while their blocks fit the GPU about once, else 4
+  const bool few = div_up(o, mx_cols(16)) * ep.max_groups <= 4 * sm_count();
+  const dim3 grid(static_cast<unsigned>(div_up(o, mx_cols(few ? 16 : 4))), static_cast<unsigned>(ep.max_groups + 1));
   LaunchScope ls(QLORA_KERNEL_TGEMM, st);
-  return y_dtype == QLORA_DTYPE_BF16 ? launch_dependent(multi_expand_kernel<true>, grid, MX_THREADS, 0, st, ep, v)
-                                     : launch_dependent(multi_expand_kernel<false>, grid, MX_THREADS, 0, st, ep, v);
+  if (y_dtype == QLORA_DTYPE_BF16)
+    return few ? launch_dependent(multi_expand_kernel<true, 16>, grid, MX_THREADS, 0, st, ep, v)
+               : launch_dependent(multi_expand_kernel<true, 4>, grid, MX_THREADS, 0, st, ep, v);
+  return few ? launch_dependent(multi_expand_kernel<false, 16>, grid, MX_THREADS, 0, st, ep, v)
+             : launch_dependent(multi_expand_kernel<false, 4>, grid, MX_THREADS, 0, st, ep, v);
 }
 
 int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlora_adapters_t* ad, int64_t o,
@@ -1845,34 +1871,19 @@ int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlo
   p.rp = static_cast<int>(rp);
   const int n_tiles = p.rp / MD_BN;
   p.tiles0 = static_cast<int>(div_up(h, MD_BM)) * n_tiles;
-  const int tiles = p.tiles0 + static_cast<int>(div_up(o, MD_BM)) * n_tiles;
-  // CTAs on a group: as many as fill the GPU (two an SM) about once, up to eight
-  const int64_t items = static_cast<int64_t>(tiles) * (ad->n < M ? ad->n : M);
-  int split = 1;
-  while (split < 8 && items * split * 2 <= 3 * sm_count() && split * MD_BK < M) split *= 2;
-  auto launch = [&](auto kernel) {
-    if (set_smem(kernel, MD_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(ad->n));
-    cfg.blockDim = dim3(MD_THREADS);
-    cfg.dynamicSmemBytes = MD_SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    LaunchScope ls(QLORA_KERNEL_TGEMM, st);
-    return cudaLaunchKernelEx(&cfg, kernel, mx, mxs, md, mds, mu, mt, p, v) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-  };
-  return split == 1   ? launch(multi_grad_kernel<1>)
-         : split == 2 ? launch(multi_grad_kernel<2>)
-         : split == 4 ? launch(multi_grad_kernel<4>)
-                      : launch(multi_grad_kernel<8>);
+  p.tiles = p.tiles0 + static_cast<int>(div_up(o, MD_BM)) * n_tiles;
+  p.n = ad->n;
+  p.split = grad_split(M, ad->n, p.tiles);
+  p.partial = w.Gpart;
+  p.counters = w.Gcnt;
+  if (p.split > 1 &&
+      cudaMemsetAsync(w.Gcnt, 0, static_cast<size_t>(p.tiles) * p.n * 4, st) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  if (set_smem_once<multi_grad_kernel>(MD_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(p.tiles) * p.n * p.split;
+  LaunchScope ls(QLORA_KERNEL_TGEMM, st);
+  return launch_dependent(multi_grad_kernel, dim3(static_cast<unsigned>(items < sm_count() ? items : sm_count())),
+                          MD_THREADS, MD_SMEM, st, mx, mxs, md, mds, mu, mt, p, v);
 }
 
 int check_multi_args(const qlora_nf4_t* Wq, int64_t M, const qlora_adapters_t* ad, int dtype, const void* plan,
