@@ -457,12 +457,19 @@ struct PackParams {
   const float* s;   // [n]
   int r, rp, parts;
   int max_slots;
+  unsigned* zero[2];  // arrival counters of the kernels that follow, set to 0
+  int zero_len[2];
 };
 
 __global__ void __launch_bounds__(256) multi_pack_kernel(const PackParams p, const PlanView v) {
   const PackJob job = blockIdx.z == 0 ? p.job[0] : p.job[1];
   const int slot = blockIdx.x;
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    pdl_wait();
+    for (int k = 0; k < 2; ++k)
+      for (int i = threadIdx.x; i < p.zero_len[k]; i += blockDim.x) p.zero[k][i] = 0;
+  }
   if (slot >= p.max_slots) {
     pdl_wait();
     if (!job.T) return;
@@ -1175,9 +1182,10 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
 // MD_CHAIN blocks (two accumulators, so that the MMAs go on) and store a finished
 // tile.  The chain is short because the tensor core cuts its running sum to fp32
 // at every step: error of dL2 against 64 bits, 4096 tokens in 4 groups, 2e-6 with
-// a group in one chain, GRADERR so (an fp32 product's is 7e-7).  One CTA for each
-// tile and group took 31 us there and 88 us for 8190 tokens, 5120 x 13824, most of
-// it the start and end of blocks that hold two stages; GRAD4096 and GRAD8190 so.
+// a group in one chain, 4e-7 so (an fp32 product's is 7e-7).  One CTA for each
+// tile and group spent most of its time on the start and end of CTAs with two
+// stages: the whole backward took 173 us there and 1065 us for 8190 tokens, 5120 x
+// 13824, with it, and takes 167 and 1023 us so.
 // When the tiles are fewer than the SMs a group's blocks are dealt to `split`
 // items, whose sums go to the partial buffer and are added in order by the one
 // that ends last.  No sum depends on timing; adapters without tokens get zeros.

@@ -1223,17 +1223,19 @@ constexpr int kMaxTensors = 1 << 20;
 template <bool k8, typename G>
 int launch_multi_adamw(const MultiAdamWParams& a, const GradPtrs& gp, int64_t blocks, cudaStream_t st) {
   const int64_t ctas = (blocks + MA_WARPS - 1) / MA_WARPS;
-  const int64_t norm = a.clip ? (ctas < MA_NORM_CTAS ? ctas : MA_NORM_CTAS) : 1;
+  const int64_t most = static_cast<int64_t>(sm_count()) * (k8 ? MA_PER_SM8 : MA_PER_SM32);
+  int64_t grid = ctas < most ? ctas : most;
+  if (grid > MA_NORM_CTAS) grid = MA_NORM_CTAS;
+  const int64_t norm = a.clip ? grid : 1;  // the update's ranges: see multi_adamw_kernel
   {
     LaunchScope ls(QLORA_KERNEL_OPTIM, st);
     multi_adamw_prepare_kernel<G><<<static_cast<unsigned>(norm), MA_THREADS, 0, st>>>(a, gp);
   }
   if (launch_status() != QLORA_OK) return QLORA_ERR_CUDA;
-  const int64_t most = static_cast<int64_t>(sm_count()) * (k8 ? MA_PER_SM8 : MA_PER_SM32);
   LaunchScope ls(QLORA_KERNEL_OPTIM, st);
   // programmatic dependent launch: the update's blocks are set up while the norm is summed
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(MA_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1544,6 +1546,7 @@ struct MultiWs {
   unsigned* Wcnt;
   float* Gpart;    // partial sums of the gradients (groups in parts)
   unsigned* Gcnt;
+  int n_wcnt, n_gcnt;
   size_t bytes;
 };
 
@@ -1576,11 +1579,13 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   // partial sums: a place for every pair, two where the pairs share all tiles evenly
   const int64_t units = div_up(M, PG_BM) * div_up(bwd ? h : o, PG_BN);
   w.Wpart = static_cast<float*>(take((units < pairs ? 2 : 1) * pairs * PG_BM * PG_BN * 4));
+  w.n_wcnt = static_cast<int>(pairs * 8);
   w.Wcnt = static_cast<unsigned*>(take(pairs * 8 * 4));
   if (bwd) {
     const int64_t items = grad_tiles(o, h, r) * n, split = grad_split(M, n, grad_tiles(o, h, r));
     if (split > 1) {
       w.Gpart = static_cast<float*>(take(items * split * MD_BM * MD_BN * 4));
+      w.n_gcnt = static_cast<int>(items);
       w.Gcnt = static_cast<unsigned*>(take(items * 4));
     }
   }
@@ -1669,8 +1674,8 @@ int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, cons
   return launch_shrink_as<128, kKN>(p, splits, v, first, st);
 }
 
-int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int parts, const PlanView& v,
-                cudaStream_t st) {
+int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int parts, const MultiWs& w,
+                const PlanView& v, cudaStream_t st) {
   PackParams p{};
   p.job[0] = j0;
   if (j1) p.job[1] = *j1;
@@ -1679,6 +1684,10 @@ int launch_pack(const PackJob& j0, const PackJob* j1, const float* s, int r, int
   p.rp = rank_pad(r);
   p.parts = parts;
   p.max_slots = static_cast<int>(max_slots(v.M, v.n));
+  p.zero[0] = w.Wcnt;
+  p.zero_len[0] = w.n_wcnt;
+  p.zero[1] = w.Gcnt;
+  p.zero_len[1] = w.n_gcnt;
   const int64_t x = p.max_slots + div_up(v.M, MP_SLOT_ROWS);
   LaunchScope ls(QLORA_KERNEL_AUX, st);
   return launch_dependent(multi_pack_kernel, dim3(static_cast<unsigned>(x), MP_SLOT_ROWS / 64, j1 ? 2 : 1), 256, 0, st,
@@ -1749,8 +1758,6 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.bank = static_cast<const uint16_t*>(kBwd ? ad->L1 : ad->L2);
   p.K = static_cast<int>(K);
   p.r = ad->r;
-  if (split > 1 && cudaMemsetAsync(w.Wcnt, 0, static_cast<size_t>(tail) * 8 * 4, st) != cudaSuccess)
-    return QLORA_ERR_CUDA;
   // even shares: a pair for every two main stages, as far as there are pairs
   const int64_t most = static_cast<int64_t>(p.g.units) * p.g.k_main_stages / 2;
   const int clusters = !p.even || most >= pairs ? pairs : static_cast<int>(most > 1 ? most : 1);
@@ -1876,9 +1883,6 @@ int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlo
   p.split = grad_split(M, ad->n, p.tiles);
   p.partial = w.Gpart;
   p.counters = w.Gcnt;
-  if (p.split > 1 &&
-      cudaMemsetAsync(w.Gcnt, 0, static_cast<size_t>(p.tiles) * p.n * 4, st) != cudaSuccess)
-    return QLORA_ERR_CUDA;
   if (set_smem_once<multi_grad_kernel>(MD_SMEM) != QLORA_OK) return QLORA_ERR_CUDA;
   const int64_t items = static_cast<int64_t>(p.tiles) * p.n * p.split;
   LaunchScope ls(QLORA_KERNEL_TGEMM, st);
@@ -1955,7 +1959,7 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   j.T = T_save;
   j.slots = w.ST;
   j.splits = shrink_splits(M, ad->n, h);
-  rc = launch_pack(j, nullptr, ad->s, r, 2, v, st);
+  rc = launch_pack(j, nullptr, ad->s, r, 2, w, v, st);
   if (rc != QLORA_OK) return rc;
   return launch_multi_pair<false>(X, w.Xs, w.ST, ad, w.Wd, o, h, 2, Y, y_dtype == QLORA_DTYPE_BF16, w, v, st);
 }
@@ -1989,7 +1993,7 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   jt.given = T_saved;
   jt.slots = w.ST;
   jt.splits = shrink_splits(M, ad->n, h);
-  rc = launch_pack(ju, &jt, ad->s, r, MD_PARTS, v, st);
+  rc = launch_pack(ju, &jt, ad->s, r, MD_PARTS, w, v, st);
   if (rc != QLORA_OK) return rc;
   rc = launch_multi_pair<true>(dY, w.Ds, w.SU, ad, w.Wd, o, h, MD_PARTS, dX, dx_dtype == QLORA_DTYPE_BF16, w, v, st);
   if (rc != QLORA_OK) return rc;
