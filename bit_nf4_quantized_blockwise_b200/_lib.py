@@ -602,6 +602,15 @@ def _check_multi(Wq: NF4Weight, bank: AdapterBank, plan: AdapterPlan, X, *rest):
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 
 
+def _workspace(ws: Optional[torch.Tensor], size: int, dev: torch.device) -> torch.Tensor:
+    """The caller's workspace if it is large enough, or a new one."""
+    if ws is None or ws.numel() * ws.element_size() < size:
+        return torch.empty(size, dtype=torch.uint8, device=dev)
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    return ws
+
+
 def _or_null(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -620,9 +629,7 @@ def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, pl
     if T_save is None and save_T:
         T_save = torch.empty(M, r, dtype=torch.float32, device=dev)
     L = lib()
-    wsb = L.qlora_multi_linear_fwd_workspace_size(Wq.o, Wq.h, M, n, r)
-    if ws is None or ws.numel() * ws.element_size() < wsb:
-        ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    ws = _workspace(ws, L.qlora_multi_linear_fwd_workspace_size(Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_fwd, "qlora_multi_linear_fwd", dev, Wq.struct(), X.data_ptr(), M, bank.struct(),
           plan.buffer.data_ptr(), plan.buffer.numel(), Y.data_ptr(), _dtype_code(Y.dtype), _or_null(T_save),
           ws.data_ptr(), ws.numel() * ws.element_size())
@@ -645,9 +652,7 @@ def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, ban
     if dL2 is None:
         dL2 = torch.empty(n, r, Wq.o, dtype=torch.float32, device=dev)
     L = lib()
-    wsb = L.qlora_multi_linear_bwd_workspace_size(Wq.o, Wq.h, M, n, r)
-    if ws is None or ws.numel() * ws.element_size() < wsb:
-        ws = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    ws = _workspace(ws, L.qlora_multi_linear_bwd_workspace_size(Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_bwd, "qlora_multi_linear_bwd", dev, Wq.struct(), X.data_ptr(), dY.data_ptr(), M,
           bank.struct(), plan.buffer.data_ptr(), plan.buffer.numel(), _or_null(T_saved), dX.data_ptr(),
           _dtype_code(dX.dtype), dL1.data_ptr(), dL2.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())

@@ -245,7 +245,7 @@ struct SortParams {
 __global__ void __launch_bounds__(256) multi_sort_rows_kernel(const SortParams p, const PlanView v) {
   pdl_launch_dependents();
   pdl_wait();
-  if (v.head->in_order) return;
+  if (__ldg(&v.head->in_order)) return;
   const bool second = blockIdx.y == 1;
   const uint4* src = second ? p.src[1] : p.src[0];
   uint4* dst = second ? p.dst[1] : p.dst[0];
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256) multi_sort_rows_kernel(const SortParams p
   for (int64_t q = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; q < all;
        q += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t p0 = q / vecs;
-    dst[q] = __ldg(src + static_cast<int64_t>(v.perm[p0]) * vecs + (q - p0 * vecs));
+    dst[q] = __ldg(src + static_cast<int64_t>(__ldg(v.perm + p0)) * vecs + (q - p0 * vecs));
   }
 }
 

@@ -1737,10 +1737,14 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.out = out;
   p.g.out_bf16 = out_bf16;
   p.g.ld_out = N;
-  p.even = p.g.units < pairs ? 1 : 0;
+  // Fewer tiles than pairs: even shares, unless they save fewer stages of the longest tile than the
+  // reduction that they need costs (about 8 us, a stage 0.84; a tile has at most one stage for each
+  // group and 64 ranks).
+  const int64_t longest = p.g.k_main_stages + (rp / 64) * (v.n < M ? v.n : (M < PG_BM ? M : PG_BM));
+  p.even = p.g.units < pairs && longest * (pairs - p.g.units) / pairs > 10 ? 1 : 0;
   // With whole rounds, the tiles of the last one, which would leave pairs without work, are split
   // along K into up to four parts (each at least two stages) that run first.
-  const int tail = p.even ? 0 : p.g.units % pairs;
+  const int tail = p.g.units < pairs ? 0 : p.g.units % pairs;
   int split = tail > 0 ? pairs / tail : 1;
   if (split > 4) split = 4;
   if (split > p.g.k_main_stages / 2) split = p.g.k_main_stages / 2;
@@ -1758,9 +1762,10 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.bank = static_cast<const uint16_t*>(kBwd ? ad->L1 : ad->L2);
   p.K = static_cast<int>(K);
   p.r = ad->r;
-  // even shares: a pair for every two main stages, as far as there are pairs
+  // even shares: a pair for every two main stages, as far as there are pairs; else one a tile
   const int64_t most = static_cast<int64_t>(p.g.units) * p.g.k_main_stages / 2;
-  const int clusters = !p.even || most >= pairs ? pairs : static_cast<int>(most > 1 ? most : 1);
+  int clusters = !p.even || most >= pairs ? pairs : static_cast<int>(most > 1 ? most : 1);
+  if (!p.even && p.g.units < clusters) clusters = p.g.units;
   {
     LaunchScope ls(kBwd ? QLORA_KERNEL_FUSED_BWD : QLORA_KERNEL_FUSED_FWD, st);
     if (launch_dependent(multi_pair_kernel<kBwd>, dim3(static_cast<unsigned>(2 * clusters)), PG_THREADS, MG_PAIR_SMEM, st,

@@ -28,7 +28,8 @@ _device, _contiguous, _data_ptr = torch.Tensor.get_device, torch.Tensor.is_conti
 class MultiAdamW:
     """AdamW over a list of fp32 CUDA tensors, updated in place.
 
-    params: contiguous fp32 tensors of one device, none of them empty;
+    params: contiguous fp32 tensors of one device, none of them empty and no two
+    of them overlapping; their memory is used until the optimizer is dropped;
     copies (optional): one bf16 tensor per parameter, or None, written with the
     rounded parameter after each step (the factors the layer reads).
     state_bits: 32, or 8 (E4M3 codes of m and of sqrt(v) with one fp32 scale per
@@ -60,6 +61,11 @@ class MultiAdamW:
             if c is not None and (c.dtype != torch.bfloat16 or c.shape != p.shape or not c.is_contiguous() or
                                   c.device != p.device):
                 raise ValueError(f"copies[{i}] must be a contiguous bf16 tensor shaped like its parameter")
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size())
+                       for p in self.params + [c for c in self.copies if c is not None])
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("params and copies overlap in memory")
         self.cfg, self.state_bits = cfg, state_bits
         self.device = self.params[0].device
         self._numel = [p.numel() for p in self.params]

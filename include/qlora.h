@@ -285,9 +285,11 @@ int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, siz
  * qlora_multi_linear_*_workspace_size() bytes.
  * W' is bf16; products are bf16 x bf16 accumulated in fp32.  T and U stay in
  * fp32 and enter the W' product as two bf16 parts (16 bits), the gradients as
- * three (24 bits); sums are added in a fixed order, so results repeat bit for
- * bit.  A token's outputs depend on its own row and adapter alone, and an
- * adapter's gradients on its own tokens alone, infinities and NaN included.  */
+ * three (24 bits).  Sums are added in a fixed order and results repeat bit for
+ * bit, except Y of up to 32 tokens (decode), whose base product is accumulated
+ * with fp32 atomics as in qlora_linear_fwd.  A token's outputs depend on its own
+ * row and adapter alone, and an adapter's gradients on its own tokens alone,
+ * infinities and NaN included.                                              */
 size_t qlora_multi_linear_fwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
 size_t qlora_multi_linear_bwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
 int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, const qlora_adapters_t* adapters,

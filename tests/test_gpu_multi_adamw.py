@@ -282,6 +282,11 @@ def test_refusals_on_the_device():
             opt.step(bad)
     with pytest.raises(ValueError):
         opt.evict()
+    buf = torch.zeros(64, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        MultiAdamW([buf[:40], buf[39:]])
+    with pytest.raises(ValueError, match="overlap"):
+        MultiAdamW([buf, buf])
     with pytest.raises(ValueError):
         opt.load_state({"m": opt.m, "v": opt.v})
     assert opt.steps.tolist() == [0]

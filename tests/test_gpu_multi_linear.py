@@ -186,6 +186,18 @@ def test_ranks(r):
     check(Case(140, 256, 512, 4, r, kind="mixed", none=0.1, seed=r), saved=False)
 
 
+@pytest.mark.parametrize("M", [1, 8, 16, 17, 32])
+@pytest.mark.parametrize("h,o,r", [(64, 256, 8), (192, 256, 72), (128, 1152, 256), (2048, 128, 64), (4096, 320, 16)])
+def test_decode_shapes(M, h, o, r):
+    check(Case(M, h, o, 5, r, kind="mixed", none=0.2, seed=M + r))
+
+
+@pytest.mark.parametrize("M,h,o,n", [(34, 64, 256, 2), (260, 2048, 128, 3), (40, 4096, 64, 40), (1025, 64, 512, 2),
+                                     (256, 512, 9728, 2)])
+def test_narrow_and_wide_layers(M, h, o, n):
+    check(Case(M, h, o, n, 8, kind="mixed", none=0.1, seed=M + h))
+
+
 @pytest.mark.parametrize("M,n,kind", [(300, 300, "each"), (700, 90, "mixed"), (1300, 1, "runs"), (1290, 6, "runs"),
                                       (64, 200, "mixed"), (16, 16, "each"), (32, 5, "mixed")])
 def test_group_sizes(M, n, kind):

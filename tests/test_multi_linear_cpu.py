@@ -126,4 +126,7 @@ def test_binding_refusals(L):
     _raises(b, _weight(), X, dY, bank, plan, dL2=torch.zeros(N, R, O, dtype=BF), match="dL2 has dtype")
     _raises(b, _weight(), X, dY, bank, plan, T_saved=torch.zeros(M + 1, R), match="T has shape")
     _raises(b, _weight(), X, dY, bank, plan, match="CUDA")
+    from bit_nf4_quantized_blockwise_b200._lib import _workspace
+    with pytest.raises(ValueError, match="ws must be"):
+        _workspace(torch.zeros(64, dtype=torch.uint8), 64, torch.device("cuda", 0))
     assert q.qlora_launch_count() == n0
