@@ -949,6 +949,11 @@ __device__ __forceinline__ bool slot_free_wait(uint64_t* done, int n, int tag) {
   return mbar_wait(&done[b % SK_NDONE], ((b / SK_NDONE) & 1) ^ 1, tag);
 }
 
+// kSeg: units after which a segment ends inside a tile too (0: only with the tile
+// or the CTA's range).  The tensor core cuts its running sum to fp32 at every
+// step; short segments are added up by the fp32 atomics instead (29 tokens, K =
+// 8192: error against 64 bits 2.8e-6 with whole tiles, SEGERR with 16 units).
+template <int kSeg>
 __global__ void __launch_bounds__(SK_THREADS, 1)
     small_m_fwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC,
                        const __grid_constant__ CUtensorMap tmL2x, const __grid_constant__ CUtensorMap tmTT,
@@ -1058,8 +1063,9 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
       int n = 0, k = c0.k, ext = 0;
       RingPos<SK_CSTAGES> rp;
       bool ok = true;
-      for (int seg = 0; n < n_units && ok; ++seg, k = 0) {
-        const int seg_end = k + (S_t - k < n_units - n ? S_t - k : n_units - n);  // one past the last k
+      for (int seg = 0; n < n_units && ok; ++seg, k = k == S_t ? 0 : k) {
+        int seg_end = k + (S_t - k < n_units - n ? S_t - k : n_units - n);  // one past the last k
+        if (kSeg > 0 && seg_end > (k / (kSeg > 0 ? kSeg : 1) + 1) * kSeg) seg_end = (k / (kSeg > 0 ? kSeg : 1) + 1) * kSeg;
         if (seg >= 2 && !mbar_wait(&acce[seg & 1], ((seg >> 1) - 1) & 1, 5)) break;
         const uint32_t d = tmem + static_cast<uint32_t>(seg & 1) * 32u;
         const int main_end = seg_end < p.k_units ? seg_end : p.k_units;
@@ -1213,8 +1219,9 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
     UnitCursor cur;
     cur.init(u0, S_t);
     for (int n = 0; n < n_units; ++n, cur.next()) {
-      if (n == 0 || cur.k == 0) ++seg;
-      const bool last = (n == n_units - 1) || (cur.k == S_t - 1);
+      const bool inner = kSeg > 0;  // segments end inside a tile too
+      if (n == 0 || cur.k == 0 || (inner && cur.k % (kSeg > 0 ? kSeg : 1) == 0)) ++seg;
+      const bool last = (n == n_units - 1) || (cur.k == S_t - 1) || (inner && (cur.k + 1) % (kSeg > 0 ? kSeg : 1) == 0);
       if (!last) continue;
       const int buf = seg & 1;
       if (!warp_wait_sleep(&accf[buf], (seg >> 1) & 1, 11)) break;

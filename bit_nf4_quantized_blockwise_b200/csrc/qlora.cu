@@ -867,10 +867,10 @@ int linear_fwd_impl(const qlora_nf4_t* Wq, const void* X, int64_t M, const void*
     sp.out = acc;
     std::memcpy(sp.codebook, Wq->codebook, sizeof(sp.codebook));
     const int64_t grid = sp.units < sm_count() ? sp.units : sm_count();
-    if (set_smem(small_m_fwd_kernel, SK_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+    if (set_smem(small_m_fwd_kernel<0>, SK_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
     {
       LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
-      small_m_fwd_kernel<<<static_cast<unsigned>(grid), SK_THREADS, SK_SMEM_BYTES, st>>>(mx, mc, ml2, mtt, sp);
+      small_m_fwd_kernel<0><<<static_cast<unsigned>(grid), SK_THREADS, SK_SMEM_BYTES, st>>>(mx, mc, ml2, mtt, sp);
     }
     if (y_dtype == QLORA_DTYPE_BF16) {
       LaunchScope ls(QLORA_KERNEL_AUX, st);
@@ -1839,9 +1839,9 @@ int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapte
     sp.absmax32 = Wq->absmax;
     sp.out = acc;
     std::memcpy(sp.codebook, Wq->codebook, sizeof(sp.codebook));
-    if (set_smem(small_m_fwd_kernel, SK_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+    if (set_smem_once<small_m_fwd_kernel<16>>(SK_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
     LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
-    small_m_fwd_kernel<<<static_cast<unsigned>(sp.units < sm_count() ? sp.units : sm_count()), SK_THREADS,
+    small_m_fwd_kernel<16><<<static_cast<unsigned>(sp.units < sm_count() ? sp.units : sm_count()), SK_THREADS,
                          SK_SMEM_BYTES, st>>>(mx, mc, mx, mx, sp);
     rc = launch_status();
   }
