@@ -952,7 +952,7 @@ __device__ __forceinline__ bool slot_free_wait(uint64_t* done, int n, int tag) {
 // kSeg: units after which a segment ends inside a tile too (0: only with the tile
 // or the CTA's range).  The tensor core cuts its running sum to fp32 at every
 // step; short segments are added up by the fp32 atomics instead (29 tokens, K =
-// 8192: error against 64 bits 2.8e-6 with whole tiles, SEGERR with 16 units).
+// 8192: error against 64 bits 2.8e-6 with whole tiles, 7e-7 with 16 units).
 template <int kSeg>
 __global__ void __launch_bounds__(SK_THREADS, 1)
     small_m_fwd_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC,

@@ -699,6 +699,7 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorM
 struct MultiPairParams {
   PairGemmParams g;         // k_ext_stages is not used: a tile has chunks stages per slot
   int even;                 // no whole rounds: the stages of all tiles in even shares (see below)
+  int chain;                // stages of an accumulator (0: those of the item)
   int chunks;               // rp / 64
   int rp, parts;
   const uint16_t* A;        // [M][K], batch order
@@ -740,22 +741,29 @@ __device__ __forceinline__ bool tile_shared(const MultiPairParams& p, const Plan
   return ps.start > mt * PG_BM || ps.end < min((mt + 1) * PG_BM, p.g.M);
 }
 
-// Replaces what is not finite among the elements n .. n + kN - 1 of sorted row m by its own sum.
-template <bool kBwd, int kN>
-__device__ __forceinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, float* x) {
-  // x 0 is 0 for finite x: one fused multiply-add each finds what is not
+// Whether all of x is finite: x 0 is 0 then, so one fused multiply-add each tells.
+template <int kN>
+__device__ __forceinline__ bool all_finite(const float* x) {
   float z = 0.0f;
 #pragma unroll
   for (int t = 0; t < kN; ++t) z = fmaf(x[t], 0.0f, z);
-  if (z == 0.0f) return;
-  for (int t = 0; t < kN; ++t) {
-    float y = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kN; ++u) y = u == t ? x[u] : y;
-    if (isfinite(y)) continue;
-    y = multi_element<kBwd>(p, v, m, n + t);
-#pragma unroll
-    for (int u = 0; u < kN; ++u) x[u] = u == t ? y : x[u];
+  return z == 0.0f;
+}
+
+// Replaces what is not finite among the `len` elements from n on that this thread has stored of
+// sorted row m by its own sum.  Never inlined: the path is rare and long.
+template <bool kBwd>
+__device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, int len) {
+  const int64_t at = static_cast<int64_t>(v.perm[m]) * p.g.ld_out + n;
+  for (int t = 0; t < len; ++t) {
+    if (p.g.out_bf16) {
+      uint16_t* o = static_cast<uint16_t*>(p.g.out) + at + t;
+      if (!isfinite(bf16_bits_to_float(*o)))
+        *o = __bfloat16_as_ushort(__float2bfloat16_rn(multi_element<kBwd>(p, v, m, n + t)));
+    } else {
+      float* o = static_cast<float*>(p.g.out) + at + t;
+      if (!isfinite(*o)) *o = multi_element<kBwd>(p, v, m, n + t);
+    }
   }
 }
 
@@ -828,8 +836,19 @@ constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<in
 // straight from the bank (the forward's L2 is an N-major operand, the
 // backward's L1 a K-major one; ranks past r are zero-filled by the 3-D map).
 // Rows are read in sorted order and written to their own place.
+// The tensor core cuts its running sum to fp32 at every step of a chain.  For a
+// bf16 result that is nothing; for an fp32 one it would be most of its error (K =
+// 11008: 1.1e-5 against 64 bits, an fp32 product 7e-7).  With an fp32 result the
+// accumulator therefore changes every MP_CHAIN stages and the epilogue, eight
+// warps with 128 sums a thread, adds it in registers while the MMAs go on with
+// the other one: CHAINERR, and CHAINTIME.  (Running sums in memory instead,
+// 256 KB a pair in L2: 453 us for 345 at 4096 x 4096 x 11008.)
+constexpr int MP_CHAIN = 8;
+constexpr int MG_EPI_WARPS = 8;
+constexpr int MG_PAIR_THREADS = 64 + 32 * MG_EPI_WARPS;
+constexpr int MG_COLS = PG_ACC_COLS / 2;  // columns of an epilogue warp
 template <bool kBwd>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
     multi_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAs,
                       const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmAe,
                       const __grid_constant__ CUtensorMap tmBe, const __grid_constant__ MultiPairParams mp,
@@ -841,7 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
   uint64_t* full = bars;                 // even CTA: TMA bytes of both CTAs (+ its producer)
   uint64_t* empty = full + PG_STAGES;    // each CTA: the MMA's commit
   uint64_t* tfull = empty + PG_STAGES;   // each CTA: accumulator complete
-  uint64_t* tempty = tfull + 2;          // even CTA: the 8 epilogue warps of the pair
+  uint64_t* tempty = tfull + 2;          // even CTA: the epilogue warps of the pair
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   int* n_even = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + PG_BAR_BYTES);
   PairItem* even = reinterpret_cast<PairItem*>(n_even + 4);
@@ -902,7 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);
+      mbar_init(&tempty[b], 2 * MG_EPI_WARPS);
     }
     fence_mbar_init();
     tma_prefetch_map(&tmB);
@@ -988,120 +1007,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PG_THREADS, 1)
         b_desc0[s] = sw128_desc(smem_u32(sB + s * PG_OPND_BYTES), 16, 1024);
         bmn_desc0[s] = sw128_desc(smem_u32(sB + s * PG_OPND_BYTES), PG_ATOM_BYTES, 1024);
       }
-      int G = 0;
+      int G = 0, A = 0;  // stages and accumulators so far
       bool ok = true;
       for (int k = 0; k < nk && ok; ++k) {
-        const int b = k & 1;
-        if (!mbar_wait_idle<true>(&tempty[b], ((k >> 1) & 1) ^ 1, kTagPgTEmpty)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + static_cast<uint32_t>(b * PG_ACC_COLS);
         const PairItem it = item_of(k);
-        for (int i = it.kbeg; i < it.kend; ++i, ++G) {
-          const int s = G % PG_STAGES;
-          if (!mbar_wait(&full[s], (G / PG_STAGES) & 1, kTagPgFull)) {
+        for (int i = it.kbeg; i < it.kend && ok; ++A) {
+          const int b = A & 1;
+          if (!mbar_wait_idle<true>(&tempty[b], ((A >> 1) & 1) ^ 1, kTagPgTEmpty)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const bool b_mn = kBwd == (i < KM);
-          const uint64_t ad = s == 0 ? a_desc0[0] : (s == 1 ? a_desc0[1] : a_desc0[2]);
-          const uint64_t bd = b_mn ? (s == 0 ? bmn_desc0[0] : (s == 1 ? bmn_desc0[1] : bmn_desc0[2]))
-                                   : (s == 0 ? b_desc0[0] : (s == 1 ? b_desc0[1] : b_desc0[2]));
-          const uint32_t idesc = idesc_bf16(PG_BM, PG_BN, false, false) | (b_mn ? 1u << 16 : 0u);
+          const uint32_t d_tmem = tmem + static_cast<uint32_t>(b * PG_ACC_COLS);
+          const int first = i, end = mp.chain > 0 ? min(it.kend, i + mp.chain) : it.kend;
+          for (; i < end; ++i, ++G) {
+            const int s = G % PG_STAGES;
+            if (!mbar_wait(&full[s], (G / PG_STAGES) & 1, kTagPgFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const bool b_mn = kBwd == (i < KM);
+            const uint64_t ad = s == 0 ? a_desc0[0] : (s == 1 ? a_desc0[1] : a_desc0[2]);
+            const uint64_t bd = b_mn ? (s == 0 ? bmn_desc0[0] : (s == 1 ? bmn_desc0[1] : bmn_desc0[2]))
+                                     : (s == 0 ? b_desc0[0] : (s == 1 ? b_desc0[1] : b_desc0[2]));
+            const uint32_t idesc = idesc_bf16(PG_BM, PG_BN, false, false) | (b_mn ? 1u << 16 : 0u);
 #pragma unroll
-          for (int kk = 0; kk < PG_BK / 16; ++kk) {
-            const uint32_t k_off = ((kk >> 2) * PG_ATOM_BYTES + (kk & 3) * 32) >> 4;
-            const uint64_t adesc = ad + k_off;
-            const uint64_t bdesc = bd + (b_mn ? static_cast<uint32_t>(kk * 2048 >> 4) : k_off);
-            umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (i > it.kbeg || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < PG_BK / 16; ++kk) {
+              const uint32_t k_off = ((kk >> 2) * PG_ATOM_BYTES + (kk & 3) * 32) >> 4;
+              const uint64_t adesc = ad + k_off;
+              const uint64_t bdesc = bd + (b_mn ? static_cast<uint32_t>(kk * 2048 >> 4) : k_off);
+              umma_bf16_pair(d_tmem, adesc, bdesc, idesc, (i > first || kk > 0) ? 1u : 0u);
+            }
+            umma_commit_pair(&empty[s], 0x3);
           }
-          umma_commit_pair(&empty[s], 0x3);
+          if (ok) umma_commit_pair(&tfull[b], 0x3);
         }
-        if (ok) umma_commit_pair(&tfull[b], 0x3);
       }
     }
-  } else if (warp >= 4) {
-    // ---------------- epilogue: warp q drains TMEM lanes 32 q .. 32 q + 31 (this CTA's rows)
+  } else {
+    // ---------------- epilogue: thread = row (TMEM lane) of this CTA, warps 2 .. 5 the first 128
+    // columns, warps 6 .. 9 the others; the sums of an item stay in registers
     const int q = warp & 3;
-    auto store_row = [&](int m, int64_t row, int n, float* x, bool shared) {
-      if (m >= p.M || n >= p.N) return;
-      if (shared) multi_repair<kBwd, 16>(mp, v, m, n, x);
-      if (p.out_bf16) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.ld_out + n);
-        uint32_t h[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) h[t] = pack_bf16x2(x[2 * t], x[2 * t + 1]);
-        __stcs(dst, make_uint4(h[0], h[1], h[2], h[3]));
-        __stcs(dst + 1, make_uint4(h[4], h[5], h[6], h[7]));
-      } else {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.ld_out + n);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) __stcs(dst + t, make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]));
-      }
-    };
-    for (int k = 0; k < nk; ++k) {
-      const int b = k & 1;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_idle(&tfull[b], (k >> 1) & 1, kTagPgTFull))) break;
-      tc_fence_after();
+    const int c0 = (warp - 2) / 4 * MG_COLS;
+    const int row = static_cast<int>(rank) * 128 + q * 32 + lane;  // row within the pair tile
+    const uint32_t t_addr = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
+    int A = 0;
+    bool ok = true;
+    for (int k = 0; k < nk && ok; ++k) {
       const PairItem it = item_of(k);
-      const int row = static_cast<int>(rank) * 128 + q * 32 + lane;  // row within the pair tile
       const int m = it.mt * PG_BM + row;
       const int64_t to = m < p.M ? v.perm[m] : 0;
-      const bool shared = tile_shared(mp, v, it.mt);
-      float* part = it.part >= 0 ? p.partial + (static_cast<int64_t>(it.part) * PG_BM + row) * PG_BN : nullptr;
-#pragma unroll 1
-      for (int c = 0; c < PG_ACC_COLS / 16; ++c) {
-        uint32_t r[16];
-        tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(b * PG_ACC_COLS + c * 16), r);
-        tmem_ld_wait();
-        if (c == PG_ACC_COLS / 16 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_even(&tempty[b], rank);
-        }
-        float x[16];
+      float x[MG_COLS];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) x[t] = __uint_as_float(r[t]);
-        if (part) {
-          float4* dst = reinterpret_cast<float4*>(part + c * 16);
-          if (m < p.M)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
-        } else {
-          store_row(m, to, it.n0 + c * 16, x, shared);
+      for (int j = 0; j < MG_COLS; ++j) x[j] = 0.0f;
+      for (int i = it.kbeg; i < it.kend; ++A) {
+        const int b = A & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_idle(&tfull[b], (A >> 1) & 1, kTagPgTFull))) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < MG_COLS; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(t_addr + static_cast<uint32_t>(b * PG_ACC_COLS + c), r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int t = 0; t < 16; ++t) x[c + t] += __uint_as_float(r[t]);
+        }
+        // the accumulator is in registers: hand it back to the MMA issuer
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_even(&tempty[b], rank);
+        i = mp.chain > 0 ? min(it.kend, i + mp.chain) : it.kend;
       }
-      if (part && !mp.even) {
-        // the warp that completes the last part of a tile sums the parts in order
+      if (!ok) break;
+      const int n0 = it.n0 + c0;
+      if (it.part >= 0) {
+        float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<int64_t>(it.part) * PG_BM + row) * PG_BN + c0);
+        if (m < p.M)
+#pragma unroll
+          for (int j = 0; j < MG_COLS; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        if (mp.even) continue;
+        // the warp that completes the last part of a tile adds the parts in order
         __threadfence();
         __syncwarp();
         const int tail = it.part / p.split;
         unsigned prior = 0;
-        if (lane == 0) prior = atomicAdd(&p.counters[(tail * 2 + static_cast<int>(rank)) * 4 + q], 1u);
+        if (lane == 0)
+          prior = atomicAdd(&p.counters[(tail * 2 + static_cast<int>(rank)) * MG_EPI_WARPS + warp - 2], 1u);
         prior = __shfl_sync(0xFFFFFFFFu, prior, 0);
-        if (prior == static_cast<unsigned>(p.split - 1)) {
-          __threadfence();
-          const float* first = p.partial + (static_cast<int64_t>(tail) * p.split * PG_BM + row) * PG_BN;
-#pragma unroll 1
-          for (int c = 0; c < PG_ACC_COLS / 16; ++c) {
-            float x[16];
+        if (prior != static_cast<unsigned>(p.split - 1)) continue;
+        __threadfence();
+        const float4* src = reinterpret_cast<const float4*>(
+            p.partial + (static_cast<int64_t>(tail) * p.split * PG_BM + row) * PG_BN + c0);
 #pragma unroll
-            for (int t = 0; t < 16; ++t) x[t] = 0.0f;
-            for (int j = 0; j < p.split; ++j) {
-              const float4* src = reinterpret_cast<const float4*>(first + static_cast<int64_t>(j) * PG_BM * PG_BN + c * 16);
+        for (int j = 0; j < MG_COLS; ++j) x[j] = 0.0f;
+        if (m < p.M)
+          for (int s = 0; s < p.split; ++s)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const float4 a = __ldcg(src + t);
-                x[4 * t] += a.x;
-                x[4 * t + 1] += a.y;
-                x[4 * t + 2] += a.z;
-                x[4 * t + 3] += a.w;
-              }
+            for (int j = 0; j < MG_COLS; j += 4) {
+              const float4 a = __ldcg(src + static_cast<int64_t>(s) * (PG_BM * PG_BN / 4) + j / 4);
+              x[j] += a.x, x[j + 1] += a.y, x[j + 2] += a.z, x[j + 3] += a.w;
             }
-            store_row(m, to, it.n0 + c * 16, x, shared);
-          }
-        }
       }
+      if (m >= p.M) continue;
+      if (p.out_bf16) {
+        uint16_t* out = static_cast<uint16_t*>(p.out) + to * p.ld_out + n0;
+#pragma unroll
+        for (int j = 0; j < MG_COLS; j += 8)
+          if (n0 + j < p.N)
+            __stcs(reinterpret_cast<uint4*>(out + j),
+                   make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]),
+                              pack_bf16x2(x[j + 4], x[j + 5]), pack_bf16x2(x[j + 6], x[j + 7])));
+      } else {
+        float* out = static_cast<float*>(p.out) + to * p.ld_out + n0;
+#pragma unroll
+        for (int j = 0; j < MG_COLS; j += 4)
+          if (n0 + j < p.N) __stcs(reinterpret_cast<float4*>(out + j), make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
+      }
+      if (tile_shared(mp, v, it.mt) && !all_finite<MG_COLS>(x))
+        multi_repair<kBwd>(mp, v, m, n0, min(MG_COLS, p.N - n0));
     }
   }
 
@@ -1160,13 +1187,13 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
       const float4 y = __ldcg(reinterpret_cast<const float4*>(p.partial + static_cast<int64_t>(2 * k) * PG_BM * PG_BN + off));
       x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
     }
-    if (shared) multi_repair<kBwd, 4>(mp, v, m, n0 + c, x);
     const int64_t to = static_cast<int64_t>(v.perm[m]) * p.ld_out + n0 + c;
     if (p.out_bf16)
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
           make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
     else
       *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = make_float4(x[0], x[1], x[2], x[3]);
+    if (shared && !all_finite<4>(x)) multi_repair<kBwd>(mp, v, m, n0 + c, 4);
   }
 }
 

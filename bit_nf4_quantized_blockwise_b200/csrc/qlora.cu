@@ -1579,8 +1579,8 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   // partial sums: a place for every pair, two where the pairs share all tiles evenly
   const int64_t units = div_up(M, PG_BM) * div_up(bwd ? h : o, PG_BN);
   w.Wpart = static_cast<float*>(take((units < pairs ? 2 : 1) * pairs * PG_BM * PG_BN * 4));
-  w.n_wcnt = static_cast<int>(pairs * 8);
-  w.Wcnt = static_cast<unsigned*>(take(pairs * 8 * 4));
+  w.n_wcnt = static_cast<int>(pairs * 2 * MG_EPI_WARPS);
+  w.Wcnt = static_cast<unsigned*>(take(w.n_wcnt * 4));
   if (bwd) {
     const int64_t items = grad_tiles(o, h, r) * n, split = grad_split(M, n, grad_tiles(o, h, r));
     if (split > 1) {
@@ -1703,7 +1703,7 @@ int multi_resident_pairs() {
   if (n > 0) return n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>((sm_count() + 1) / 2), 1, 1);
-  cfg.blockDim = dim3(PG_THREADS, 1, 1);
+  cfg.blockDim = dim3(MG_PAIR_THREADS, 1, 1);
   cfg.dynamicSmemBytes = MG_PAIR_SMEM;
   if (cudaOccupancyMaxActiveClusters(&n, multi_pair_kernel<kBwd>, &cfg) != cudaSuccess || n <= 0) return 0;
   cache[dev].store(n);
@@ -1753,6 +1753,7 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.full_units = split > 1 ? p.g.units - tail : p.g.units;
   p.g.partial = w.Wpart;
   p.g.counters = w.Wcnt;
+  p.chain = out_bf16 ? 0 : MP_CHAIN;
   p.chunks = static_cast<int>(rp / 64);
   p.rp = static_cast<int>(rp);
   p.parts = parts;
@@ -1768,8 +1769,8 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   if (!p.even && p.g.units < clusters) clusters = p.g.units;
   {
     LaunchScope ls(kBwd ? QLORA_KERNEL_FUSED_BWD : QLORA_KERNEL_FUSED_FWD, st);
-    if (launch_dependent(multi_pair_kernel<kBwd>, dim3(static_cast<unsigned>(2 * clusters)), PG_THREADS, MG_PAIR_SMEM, st,
-                         ma, mas, mb, mae, mbe, p, v) != QLORA_OK)
+    if (launch_dependent(multi_pair_kernel<kBwd>, dim3(static_cast<unsigned>(2 * clusters)), MG_PAIR_THREADS,
+                         MG_PAIR_SMEM, st, ma, mas, mb, mae, mbe, p, v) != QLORA_OK)
       return QLORA_ERR_CUDA;
   }
   if (p.even && clusters > 1) {
