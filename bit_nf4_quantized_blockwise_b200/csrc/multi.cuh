@@ -841,8 +841,9 @@ constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<in
 // 11008: 1.1e-5 against 64 bits, an fp32 product 7e-7).  With an fp32 result the
 // accumulator therefore changes every MP_CHAIN stages and the epilogue, eight
 // warps with 128 sums a thread, adds it in registers while the MMAs go on with
-// the other one: CHAINERR, and CHAINTIME.  (Running sums in memory instead,
-// 256 KB a pair in L2: 453 us for 345 at 4096 x 4096 x 11008.)
+// the other one: 7.6e-7, for 371 us instead of 345 at 4096 x 4096 x 11008 (313 with a
+// bf16 result).  (Running sums in memory instead,
+// 256 KB a pair in L2: 453 us.)
 constexpr int MP_CHAIN = 8;
 constexpr int MG_EPI_WARPS = 8;
 constexpr int MG_PAIR_THREADS = 64 + 32 * MG_EPI_WARPS;
@@ -1085,10 +1086,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
       if (!ok) break;
       const int n0 = it.n0 + c0;
       if (it.part >= 0) {
-        float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<int64_t>(it.part) * PG_BM + row) * PG_BN + c0);
+        // [4 columns][row]: a warp's 32 rows are 512 contiguous bytes
+        float4* dst = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(it.part) * PG_BM * PG_BN) +
+                      c0 / 4 * PG_BM + row;
         if (m < p.M)
 #pragma unroll
-          for (int j = 0; j < MG_COLS; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          for (int j = 0; j < MG_COLS; j += 4) dst[j / 4 * PG_BM] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
         if (mp.even) continue;
         // the warp that completes the last part of a tile adds the parts in order
         __threadfence();
@@ -1100,15 +1103,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
         prior = __shfl_sync(0xFFFFFFFFu, prior, 0);
         if (prior != static_cast<unsigned>(p.split - 1)) continue;
         __threadfence();
-        const float4* src = reinterpret_cast<const float4*>(
-            p.partial + (static_cast<int64_t>(tail) * p.split * PG_BM + row) * PG_BN + c0);
+        const float4* src =
+            reinterpret_cast<const float4*>(p.partial + static_cast<int64_t>(tail) * p.split * PG_BM * PG_BN) +
+            c0 / 4 * PG_BM + row;
 #pragma unroll
         for (int j = 0; j < MG_COLS; ++j) x[j] = 0.0f;
         if (m < p.M)
           for (int s = 0; s < p.split; ++s)
 #pragma unroll
             for (int j = 0; j < MG_COLS; j += 4) {
-              const float4 a = __ldcg(src + static_cast<int64_t>(s) * (PG_BM * PG_BN / 4) + j / 4);
+              const float4 a = __ldcg(src + static_cast<int64_t>(s) * (PG_BM * PG_BN / 4) + j / 4 * PG_BM);
               x[j] += a.x, x[j + 1] += a.y, x[j + 2] += a.z, x[j + 3] += a.w;
             }
       }
@@ -1176,24 +1180,34 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
   if (c0 == c1) return;  // one pair computed the whole tile and has stored it
   const int64_t place0 = 2 * c0 + (at > stage_share(all, c0, pairs).lo ? 1 : 0);
   const bool shared = tile_shared(mp, v, mt);
-  for (int q = threadIdx.x; q < MR_ROWS * PG_BN / 4; q += 256) {
-    const int m = m0 + q / (PG_BN / 4), c = 4 * (q % (PG_BN / 4));
+  const float4* first = reinterpret_cast<const float4*>(p.partial + place0 * PG_BM * PG_BN);
+  const float4* rest = reinterpret_cast<const float4*>(p.partial);
+  // 8 columns of a row a thread; the places are [4 columns][row]
+  for (int q = threadIdx.x; q < MR_ROWS * PG_BN / 8; q += 256) {
+    const int m = m0 + q % MR_ROWS, c = 8 * (q / MR_ROWS);
     if (m >= p.M || n0 + c >= p.N) continue;
-    const int64_t off = static_cast<int64_t>(m - mt * PG_BM) * PG_BN + c;
-    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.partial + place0 * PG_BM * PG_BN + off));
-    float x[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll 4
+    const int off = c / 4 * PG_BM + m - mt * PG_BM;
+    float4 x[2] = {__ldcg(first + off), __ldcg(first + off + PG_BM)};
+#pragma unroll 2
     for (int k = c0 + 1; k <= c1; ++k) {  // the tile is the first of every further pair's share
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p.partial + static_cast<int64_t>(2 * k) * PG_BM * PG_BN + off));
-      x[0] += y.x, x[1] += y.y, x[2] += y.z, x[3] += y.w;
+      const float4* src = rest + static_cast<int64_t>(2 * k) * (PG_BM * PG_BN / 4) + off;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float4 y = __ldcg(src + u * PG_BM);
+        x[u].x += y.x, x[u].y += y.y, x[u].z += y.z, x[u].w += y.w;
+      }
     }
     const int64_t to = static_cast<int64_t>(v.perm[m]) * p.ld_out + n0 + c;
-    if (p.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + to) =
-          make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = make_float4(x[0], x[1], x[2], x[3]);
-    if (shared && !all_finite<4>(x)) multi_repair<kBwd>(mp, v, m, n0 + c, 4);
+    if (p.out_bf16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to) =
+          make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[0].z, x[0].w), pack_bf16x2(x[1].x, x[1].y),
+                     pack_bf16x2(x[1].z, x[1].w));
+    } else {
+      float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.out) + to);
+      out[0] = x[0], out[1] = x[1];
+    }
+    const float all[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    if (shared && !all_finite<8>(all)) multi_repair<kBwd>(mp, v, m, n0 + c, 8);
   }
 }
 
