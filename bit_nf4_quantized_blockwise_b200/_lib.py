@@ -245,12 +245,6 @@ def _check_linear(Wq: "NF4Weight", X, L1, L2, Y=None, T=None, dY=None, dX=None, 
     return M, r
 
 
-def _fits(t: torch.Tensor, shape, *dtypes) -> bool:
-    """What _need asks, as one cheap test: a decode call lasts a few microseconds on the device, so the
-    many-adapter calls check with this and let _need name what is wrong."""
-    return t.shape == shape and t.dtype in dtypes and t.is_contiguous()
-
-
 @functools.lru_cache(maxsize=64)
 def _codebook_of(codebook: Tuple[float, ...]):
     return _codebook_array(codebook)
@@ -521,7 +515,8 @@ class AdapterBank:
         return self.dims[2]
 
     def struct(self) -> qlora_adapters_t:
-        return qlora_adapters_t(self.L1.data_ptr(), self.L2.data_ptr(), self.s.data_ptr(), self.dims[0], self.dims[2])
+        n, _, r, _ = self.dims
+        return qlora_adapters_t(self.L1.data_ptr(), self.L2.data_ptr(), self.s.data_ptr(), n, r)
 
 
 @dataclass(frozen=True)
@@ -564,15 +559,19 @@ def _check_multi(Wq: NF4Weight, bank: AdapterBank, plan: AdapterPlan, X, *rest):
     """Every operand of the many-adapter layer against the weight, the bank and
     the plan; rest: (tensor or None, name, shape by its letters, dtypes)."""
     o, h = Wq.o, Wq.h
-    w = Wq.codes
-    if w is None or w.numel() != o * h // 2 or w.dtype is not torch.uint8 or not w.is_contiguous():
+    codes, absmax = Wq.codes, Wq.absmax
+    if absmax is not None:
         _check_weight(Wq)
-    consts = (Wq.absmax,) if Wq.absmax is not None else (Wq.absmax_fp8, Wq.dq_scale, Wq.dq_mean)
-    if Wq.absmax is not None or any(c is None for c in consts) or consts[0].numel() != o * h // 64 or \
-            consts[0].dtype is not torch.uint8 or consts[1].numel() != o * h // 16384 or \
-            consts[1].dtype is not torch.float32 or consts[2].numel() != 1 or consts[2].dtype is not torch.float32 or \
-            not (consts[0].is_contiguous() and consts[1].is_contiguous()):
-        _check_weight(Wq)
+        devs = {absmax.get_device()}
+    else:
+        fp8, scale, mean = Wq.absmax_fp8, Wq.dq_scale, Wq.dq_mean
+        if fp8 is None or scale is None or mean is None or fp8.numel() != o * h // 64 or \
+                scale.numel() != o * h // 16384 or mean.numel() != 1 or fp8.dtype is not torch.uint8 or \
+                scale.dtype is not torch.float32 or mean.dtype is not torch.float32 or not fp8.is_contiguous() or \
+                not scale.is_contiguous() or codes is None or codes.numel() != o * h // 2 or \
+                codes.dtype is not torch.uint8 or not codes.is_contiguous():
+            _check_weight(Wq)
+        devs = {fp8.get_device(), scale.get_device(), mean.get_device()}
     if X.dim() != 2 or X.shape[1] != h:
         raise ValueError(f"X has shape {tuple(X.shape)}, expected (M, {h})")
     M = X.shape[0]
@@ -581,15 +580,13 @@ def _check_multi(Wq: NF4Weight, bank: AdapterBank, plan: AdapterPlan, X, *rest):
         raise ValueError(f"the bank is for {hb} x {ob}, the weight is {h} x {o}")
     if plan.M != M or plan.n != n:
         raise ValueError(f"plan is for {plan.M} tokens and {plan.n} adapters, not {M} and {n}")
-    if not _fits(X, (M, h), torch.bfloat16):
+    if X.dtype is not torch.bfloat16 or not X.is_contiguous():
         _need(X, "X", (M, h), (torch.bfloat16,))
-    size = {"M": M, "h": h, "o": o, "n": n, "r": r}
-    devs = {X.get_device(), w.get_device(), bank.L1.get_device(), plan.buffer.get_device()}
-    devs.update([c.get_device() for c in consts])
+    devs.update((X.get_device(), codes.get_device(), bank.L1.get_device(), plan.buffer.get_device()))
     for t, name, letters, dtypes in rest:
         if t is not None:
-            shape = tuple([size[c] for c in letters])
-            if not _fits(t, shape, *dtypes):
+            shape = tuple([{"M": M, "h": h, "o": o, "n": n, "r": r}[c] for c in letters])
+            if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
                 _need(t, name, shape, dtypes)
             devs.add(t.get_device())
     if len(devs) > 1:

@@ -709,20 +709,42 @@ struct MultiPairParams {
   int K, r;
 };
 
-// One element from its own row and adapter alone, in fp32.
-template <bool kBwd>
-__device__ __noinline__ float multi_element(const MultiPairParams& p, const PlanView& v, int m, int n) {
-  const uint16_t* a = p.A + static_cast<int64_t>(v.perm[m]) * p.K;
-  float x = 0.0f;
-  for (int k = 0; k < p.K; ++k)
-    x = fmaf(bf16_bits_to_float(a[k]),
-             bf16_bits_to_float(p.Wd[kBwd ? static_cast<int64_t>(k) * p.g.N + n : static_cast<int64_t>(n) * p.K + k]), x);
+__device__ __forceinline__ float dot8(uint4 a, uint4 b, float x) {
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x = fmaf(__uint_as_float(aw[i] << 16), __uint_as_float(bw[i] << 16), x);
+    x = fmaf(__uint_as_float(aw[i] & 0xFFFF0000u), __uint_as_float(bw[i] & 0xFFFF0000u), x);
+  }
+  return x;
+}
+
+// The slot row of sorted row m, or null for a row without adapter, and its adapter.
+__device__ __forceinline__ const uint16_t* slot_row(const MultiPairParams& p, const PlanView& v, int m, int& adapter) {
   const int t = m / MP_SLOT_ROWS;
   for (int s = v.tile_slot0[t]; s < v.tile_slot0[t + 1]; ++s) {
     const PlanSlot ps = plan_load(v.slots + s);
     if (m < ps.start || m >= ps.end) continue;
-    const uint16_t* row = p.slots + (static_cast<int64_t>(s) * MP_SLOT_ROWS + m % MP_SLOT_ROWS) * (p.parts * p.rp);
-    const uint16_t* b = p.bank + static_cast<int64_t>(ps.adapter) * p.r * p.g.N;
+    adapter = ps.adapter;
+    return p.slots + (static_cast<int64_t>(s) * MP_SLOT_ROWS + m % MP_SLOT_ROWS) * (p.parts * p.rp);
+  }
+  return nullptr;
+}
+
+// One element from its own row and adapter alone, in fp32.
+template <bool kBwd>
+__device__ float multi_element(const MultiPairParams& p, const uint16_t* a, const uint16_t* row, int adapter, int n) {
+  float x = 0.0f;
+  if (kBwd) {
+    for (int k = 0; k < p.K; ++k)
+      x = fmaf(bf16_bits_to_float(a[k]), bf16_bits_to_float(p.Wd[static_cast<int64_t>(k) * p.g.N + n]), x);
+  } else {
+    const uint16_t* w = p.Wd + static_cast<int64_t>(n) * p.K;
+    for (int k = 0; k < p.K; k += 8)  // K is a multiple of 64
+      x = dot8(*reinterpret_cast<const uint4*>(a + k), *reinterpret_cast<const uint4*>(w + k), x);
+  }
+  if (row) {
+    const uint16_t* b = p.bank + static_cast<int64_t>(adapter) * p.r * p.g.N;
     float d = 0.0f;
     for (int j = 0; j < p.r; ++j) {
       const float w = bf16_bits_to_float(b[kBwd ? static_cast<int64_t>(n) * p.r + j : static_cast<int64_t>(j) * p.g.N + n]);
@@ -751,18 +773,34 @@ __device__ __forceinline__ bool all_finite(const float* x) {
 }
 
 // Replaces what is not finite among the `len` elements from n on that this thread has stored of
-// sorted row m by its own sum.  Never inlined: the path is rare and long.
+// sorted row m by its own sum; nothing to do where the row itself is not finite, or its product with
+// its adapter's first factor is NaN (then all its elements are).  So a batch of NaN costs a look at
+// its rows, and one adapter of NaN the tiles it shares with others (a few milliseconds a tile).
+// Never inlined: the path is rare and long.
 template <bool kBwd>
 __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, int len) {
+  const uint16_t* a = p.A + static_cast<int64_t>(v.perm[m]) * p.K;
+  int adapter = -1;
+  const uint16_t* row = slot_row(p, v, m, adapter);
+  if (row)
+    for (int j = 0; j < p.r; ++j)
+      if (isnan(bf16_bits_to_float(row[j]))) return;
+  for (int k = 0; k < p.K; k += 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(a + k);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // an exponent of ones in either half
+      if ((w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u) return;
+  }
   const int64_t at = static_cast<int64_t>(v.perm[m]) * p.g.ld_out + n;
   for (int t = 0; t < len; ++t) {
     if (p.g.out_bf16) {
       uint16_t* o = static_cast<uint16_t*>(p.g.out) + at + t;
       if (!isfinite(bf16_bits_to_float(*o)))
-        *o = __bfloat16_as_ushort(__float2bfloat16_rn(multi_element<kBwd>(p, v, m, n + t)));
+        *o = __bfloat16_as_ushort(__float2bfloat16_rn(multi_element<kBwd>(p, a, row, adapter, n + t)));
     } else {
       float* o = static_cast<float*>(p.g.out) + at + t;
-      if (!isfinite(*o)) *o = multi_element<kBwd>(p, v, m, n + t);
+      if (!isfinite(*o)) *o = multi_element<kBwd>(p, a, row, adapter, n + t);
     }
   }
 }
@@ -1256,8 +1294,8 @@ struct MultiGradParams {
   int tiles0;          // 128-row tiles of dL1, times the rank tiles
   int tiles;           // and of dL2
   int split;           // parts of a group's blocks
-  float* partial;      // [items][128][64]
-  unsigned* counters;  // [tiles * n], zero at launch
+  float* partial;      // [group][tile][part] sums of [64][128]
+  unsigned* counters;  // [group][tile], zero at launch
 };
 
 // One element of a factor's gradient from the group's own tokens alone, in fp32.
@@ -1295,6 +1333,7 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
   // are of different adapters
   struct Item {
     int second, m0, j0, adapter, grp;
+    int tile, part;
     int i0, blocks;  // 64-row blocks i0 .. i0 + blocks - 1 of the sorted order
     PlanGroup pg;
   };
@@ -1304,6 +1343,8 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
     const int64_t w = u / p.split;
     it.adapter = static_cast<int>(w / p.tiles);
     int tile = static_cast<int>(w - static_cast<int64_t>(it.adapter) * p.tiles);
+    it.tile = tile;
+    it.part = part;
     it.second = tile >= p.tiles0 ? 1 : 0;
     if (it.second) tile -= p.tiles0;
     it.m0 = (tile / n_tiles) * MD_BM;
@@ -1434,9 +1475,10 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
         if (lane == 0) mbar_arrive(&tempty[C & 1]);
       }
       if (!ok) break;
-      const int64_t tile_index = u / p.split;
-      if (p.split > 1) {
-        float* part = p.partial + u * (MD_BM * MD_BN) + row;  // [rank][row]: coalesced
+      if (it.grp < 0 && it.part > 0) continue;  // zeros are stored once
+      if (p.split > 1 && it.grp >= 0) {
+        const int64_t tile_index = static_cast<int64_t>(it.grp) * p.tiles + it.tile;
+        float* part = p.partial + (tile_index * p.split + it.part) * (MD_BM * MD_BN) + row;  // [rank][row]: coalesced
 #pragma unroll
         for (int j = 0; j < MD_BN; ++j) part[j * MD_BM] = x[j];
         __threadfence();

@@ -1582,7 +1582,7 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   w.n_wcnt = static_cast<int>(pairs * 2 * MG_EPI_WARPS);
   w.Wcnt = static_cast<unsigned*>(take(w.n_wcnt * 4));
   if (bwd) {
-    const int64_t items = grad_tiles(o, h, r) * n, split = grad_split(M, n, grad_tiles(o, h, r));
+    const int64_t items = grad_tiles(o, h, r) * (n < M ? n : M), split = grad_split(M, n, grad_tiles(o, h, r));
     if (split > 1) {
       w.Gpart = static_cast<float*>(take(items * split * MD_BM * MD_BN * 4));
       w.n_gcnt = static_cast<int>(items);

@@ -294,6 +294,51 @@ def test_nonfinite_values_stay_with_their_token_and_adapter(M, kind, what, value
         assert not torch.isfinite(dX[bad_row]).any()
 
 
+@pytest.mark.parametrize("M", [20, 300, 1300])
+def test_a_batch_of_nan_ends_and_keeps_to_itself(M):
+    """All of X and dY NaN but for the tokens of adapter 2, which are as before."""
+    c = Case(M, 256, 320, 3, 16, kind="mixed", none=0.1, seed=M)
+    mine = c.ids == 2
+    wY, bY, wT, bT = c.forward()
+    wX, bX, w1, b1, w2, b2 = c.backward()
+    c.X[torch.from_numpy(~mine)] = float("nan")
+    c.dY[torch.from_numpy(~mine)] = float("nan")
+    bank, plan = c.device()
+    X, dY = c.X.cuda(), c.dY.cuda()
+    Y, T = q.qlora_multi_linear_fwd(c.Wq, X, bank, plan)
+    dX, d1, d2 = q.qlora_multi_linear_bwd(c.Wq, X, dY, bank, plan, T_saved=T)
+    torch.cuda.synchronize()
+    q.qlora_check_status()
+    near(Y[mine], wY[mine], bY[mine])
+    near(dX[mine], wX[mine], bX[mine])
+    near(d1[2:], w1[2:], b1[2:])
+    near(d2[2:], w2[2:], b2[2:])
+    assert torch.isnan(Y[~mine]).all() and torch.isnan(dX[~mine]).all()
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_an_adapter_of_nan_keeps_to_its_tokens(M):
+    c = Case(M, 256, 320, 3, 16, kind="mixed", none=0.1, seed=M)
+    mine = c.ids != 1
+    wY, bY, _, _ = c.forward()
+    wX, bX, _, _, _, _ = c.backward()
+    c.L1[1] = float("nan")
+    c.L2[1] = float("inf")
+    bank, plan = c.device()
+    X, dY = c.X.cuda(), c.dY.cuda()
+    Y, _ = q.qlora_multi_linear_fwd(c.Wq, X, bank, plan, y_dtype=torch.bfloat16)
+    dX, _, _ = q.qlora_multi_linear_bwd(c.Wq, X, dY, bank, plan, dx_dtype=torch.bfloat16)
+    near(Y[mine], wY[mine], rounded(wY, bY, torch.bfloat16)[mine])
+    near(dX[mine], wX[mine], rounded(wX, bX, torch.bfloat16)[mine])
+    assert not torch.isfinite(Y[~mine]).any() and not torch.isfinite(dX[~mine]).any()
+
+
+def test_large_bank_with_few_of_its_adapters_in_the_batch():
+    c = Case(70, 128, 128, 3000, 8, kind="mixed", seed=4)
+    c.ids = np.where(c.ids % 3 == 0, 2999, c.ids % 5).astype(np.int32)
+    check(c)
+
+
 # ---------------------------------------------------------------- how it is called
 
 def test_results_repeat_bit_for_bit():
