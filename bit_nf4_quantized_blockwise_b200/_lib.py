@@ -112,7 +112,7 @@ EXPORTS = {
                                         ctypes.POINTER(qlora_adapters_t), _c_void_p, _c_size, _c_void_p, _c_void_p,
                                         _c_int, _c_void_p, _c_void_p, _c_void_p, _c_size, _c_void_p]),
     "qlora_multi_adamw_state_elems": (_c_i64, [_c_void_p, _c_int]),
-    "qlora_multi_adamw_plan_size": (_c_size, [_c_int]),
+    "qlora_multi_adamw_plan_size": (_c_size, [_c_int, _c_i64]),
     "qlora_multi_adamw_plan": (_c_int, [_c_void_p, _c_int, _c_void_p, _c_size, _c_void_p]),
     "qlora_multi_adamw_step": (_c_int, [_c_void_p, _c_size, _c_int, _c_i64, _c_void_p, _c_int, _c_void_p, _c_void_p,
                                         _c_void_p]),

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(float* __restrict__ p, const
 constexpr int MA_BLOCK = 256;
 constexpr int MA_THREADS = 256;
 constexpr int MA_WARPS = MA_THREADS / 32;
+constexpr int MA_COARSE = 64;
 // Resident CTAs of the update.  Registers for the prefetched block against
 // warps: 8 bits 722 / 705 / 751 us a step of 160 M parameters at 2 / 3 / 4 CTAs,
 // 32 bits 895 / 984 at 2 / 3.
@@ -142,6 +143,7 @@ struct MultiHead {
 struct MultiAdamWParams {
   MultiHead* head;
   MultiTensor* tensors;   // [count + 1]; the last one only closes block0
+  const int* coarse;      // tensor of every MA_COARSE-th block
   MultiCoef* coef;        // [count]
   const void** stored;    // gradient pointers in memory (lists longer than MA_PTRS)
   int count;
@@ -169,17 +171,12 @@ __device__ __forceinline__ const void* multi_grad(const MultiAdamWParams& a, con
   return a.from_memory ? a.stored[t] : gp.g[t];
 }
 
-// The tensor that holds block b: the last one with block0 <= b.
-__device__ __forceinline__ int multi_find(const MultiTensor* ts, int count, int64_t b) {
-  int lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ts[mid].block0 <= b)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
+// The tensor that holds block b: from the coarse index on (a search over the table would be a chain
+// of dependent loads at the start of every CTA).
+__device__ __forceinline__ int multi_find(const MultiAdamWParams& a, int64_t b) {
+  int t = __ldg(a.coarse + b / MA_COARSE);
+  while (a.tensors[t + 1].block0 <= b) ++t;
+  return t;
 }
 
 // A lane's 8 elements of a block: 4 lane .. 4 lane + 3 and 128 more.
@@ -228,8 +225,8 @@ __device__ __forceinline__ bool vec_ok(const void* p, int bytes) {
 }
 
 // The norm of all gradients (fp64; the partial sums of the CTAs are added in
-// order, so the norm does not depend on timing) and, in the CTA that ends
-// last, the clipping factor and each tensor's coefficients.  A tensor without
+// order, by the one that ends last, so the norm does not depend on timing), the
+// clipping factor and each tensor's coefficients.  A tensor without
 // gradient (null pointer) is left out and its step count stands.
 template <typename G>
 __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const __grid_constant__ MultiAdamWParams a,
@@ -238,11 +235,22 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
   __shared__ bool last;
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == gridDim.x - 1)  // beside the other CTAs' sums
+    for (int t = threadIdx.x; t < a.count; t += MA_THREADS) {
+      if (!multi_grad(a, gp, t)) continue;
+      const int k = ++a.steps[t];
+      MultiCoef c;
+      c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k)));
+      const double root = sqrt(1.0 - pow(static_cast<double>(a.beta2), k));
+      c.bc2_sqrt = static_cast<float>(root);
+      c.bc2_inv = static_cast<float>(1.0 / root);
+      a.coef[t] = c;
+    }
   double s = 0.0;
   if (a.clip) {
     const int64_t blocks = a.head->blocks;
     const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
-    int t = b0 < b1 ? multi_find(a.tensors, a.count, b0) : 0;
+    int t = b0 < b1 ? multi_find(a, b0) : 0;
     for (int64_t b = b0; b < b1; ++t) {
       const MultiTensor ts = a.tensors[t];
       const int64_t next = a.tensors[t + 1].block0;
@@ -282,16 +290,6 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
   __syncthreads();
   if (!last) return;
   __threadfence();
-  for (int t = threadIdx.x; t < a.count; t += MA_THREADS) {
-    if (!multi_grad(a, gp, t)) continue;
-    const int k = ++a.steps[t];
-    MultiCoef c;
-    c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k)));
-    const double root = sqrt(1.0 - pow(static_cast<double>(a.beta2), k));
-    c.bc2_sqrt = static_cast<float>(root);
-    c.bc2_inv = static_cast<float>(1.0 / root);
-    a.coef[t] = c;
-  }
   if (warp == 0) {
     double x = 0.0;
     for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) x += __ldcg(a.head->partial + i);
@@ -391,7 +389,7 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
   if (b0 >= b1) return;
   pdl_wait();  // coefficients, and the step before this one
   const float clip = __ldcg(&a.head->clip);
-  int t = multi_find(a.tensors, a.count, b1 - 1);
+  int t = multi_find(a, b1 - 1);
   for (int64_t top = b1; top > b0; --t) {
     const MultiTensor ts = a.tensors[t];
     const int64_t lo = ts.block0 > b0 ? ts.block0 : b0;

@@ -1198,10 +1198,11 @@ struct MultiPlan {
   MultiTensor* tensors;
   MultiCoef* coef;
   const void** stored;
+  int* coarse;
   size_t bytes;
 };
 
-MultiPlan multi_plan_layout(void* base, int count) {
+MultiPlan multi_plan_layout(void* base, int count, int64_t blocks) {
   uint8_t* p = static_cast<uint8_t*>(base);
   size_t off = 0;
   auto take = [&](size_t bytes) -> void* {
@@ -1214,6 +1215,7 @@ MultiPlan multi_plan_layout(void* base, int count) {
   m.tensors = static_cast<MultiTensor*>(take(sizeof(MultiTensor) * (static_cast<size_t>(count) + 1)));
   m.coef = static_cast<MultiCoef*>(take(sizeof(MultiCoef) * static_cast<size_t>(count)));
   m.stored = static_cast<const void**>(take(sizeof(void*) * static_cast<size_t>(count)));
+  m.coarse = static_cast<int*>(take(sizeof(int) * static_cast<size_t>(blocks / MA_COARSE + 1)));
   m.bytes = off;
   return m;
 }
@@ -1260,8 +1262,9 @@ int64_t qlora_multi_adamw_state_elems(const qlora_adamw_tensor_t* tensors, int c
   return blocks * MA_BLOCK;
 }
 
-size_t qlora_multi_adamw_plan_size(int count) {
-  return count < 1 || count > kMaxTensors ? 0 : multi_plan_layout(nullptr, count).bytes;
+size_t qlora_multi_adamw_plan_size(int count, int64_t state_elems) {
+  if (count < 1 || count > kMaxTensors || state_elems < MA_BLOCK) return 0;
+  return multi_plan_layout(nullptr, count, state_elems / MA_BLOCK).bytes;
 }
 
 int qlora_multi_adamw_plan(const qlora_adamw_tensor_t* tensors, int count, void* plan, size_t plan_bytes,
@@ -1275,33 +1278,31 @@ int qlora_multi_adamw_plan(const qlora_adamw_tensor_t* tensors, int count, void*
   }
   const int64_t elems = qlora_multi_adamw_state_elems(tensors, count);
   if (elems < 1) return QLORA_ERR_SHAPE;
-  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count)) return QLORA_ERR_WORKSPACE;
+  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count, elems)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(plan)) return QLORA_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(st, &cap) != cudaSuccess) return QLORA_ERR_CUDA;
   if (cap != cudaStreamCaptureStatusNone) return QLORA_ERR_UNSUPPORTED;  // a replay would read the host table again
-  MultiTensor* host = new (std::nothrow) MultiTensor[static_cast<size_t>(count) + 1];
-  MultiHead* head = new (std::nothrow) MultiHead();
-  int rc = host && head ? QLORA_OK : QLORA_ERR_WORKSPACE;
-  if (rc == QLORA_OK) {
-    const MultiPlan mp = multi_plan_layout(plan, count);
-    int64_t b = 0;
-    for (int i = 0; i < count; ++i) {
-      host[i] = {tensors[i].param, tensors[i].copy, tensors[i].n, b};
-      b += (tensors[i].n + MA_BLOCK - 1) / MA_BLOCK;
-    }
-    host[count] = {nullptr, nullptr, 0, b};
-    head->blocks = b;
-    // both copies are from pageable memory, which the calls have read when they return
-    if (cudaMemcpyAsync(mp.head, head, sizeof(MultiHead), cudaMemcpyHostToDevice, st) != cudaSuccess ||
-        cudaMemcpyAsync(mp.tensors, host, sizeof(MultiTensor) * (static_cast<size_t>(count) + 1),
-                        cudaMemcpyHostToDevice, st) != cudaSuccess)
-      rc = QLORA_ERR_CUDA;
+  const int64_t blocks = elems / MA_BLOCK;
+  const MultiPlan mp = multi_plan_layout(plan, count, blocks);
+  const size_t bytes = mp.bytes;
+  uint8_t* host = new (std::nothrow) uint8_t[bytes]();
+  if (!host) return QLORA_ERR_WORKSPACE;
+  const MultiPlan hp = multi_plan_layout(host, count, blocks);
+  int64_t b = 0;
+  for (int i = 0; i < count; ++i) {
+    hp.tensors[i] = {tensors[i].param, tensors[i].copy, tensors[i].n, b};
+    const int64_t end = b + (tensors[i].n + MA_BLOCK - 1) / MA_BLOCK;
+    for (int64_t c = (b + MA_COARSE - 1) / MA_COARSE; c * MA_COARSE < end; ++c) hp.coarse[c] = i;
+    b = end;
   }
+  hp.tensors[count] = {nullptr, nullptr, 0, b};
+  hp.head->blocks = b;
+  // from pageable memory, which the call has read when it returns
+  const bool ok = cudaMemcpyAsync(plan, host, bytes, cudaMemcpyHostToDevice, st) == cudaSuccess;
   delete[] host;
-  delete head;
-  return rc;
+  return ok ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t state_elems, const void* const* grads,
@@ -1315,7 +1316,7 @@ int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t sta
   if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f && hp->eps > 0.0f &&
         hp->lr >= 0.0f && hp->weight_decay >= 0.0f && std::isfinite(hp->max_grad_norm)))
     return QLORA_ERR_UNSUPPORTED;
-  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count)) return QLORA_ERR_WORKSPACE;
+  if (!plan || plan_bytes < qlora_multi_adamw_plan_size(count, state_elems)) return QLORA_ERR_WORKSPACE;
   if (!aligned16(plan) || !aligned16(state->m) || !aligned16(state->v)) return QLORA_ERR_ALIGN;
   const uintptr_t gmask = grad_dtype == QLORA_DTYPE_F32 ? 3u : 1u;
   bool any = false;
@@ -1325,12 +1326,13 @@ int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t sta
   }
   if (!any) return QLORA_OK;  // nothing has a gradient
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const MultiPlan mp = multi_plan_layout(plan, count);
+  const MultiPlan mp = multi_plan_layout(plan, count, state_elems / MA_BLOCK);
   MultiAdamWParams a{};
   a.head = mp.head;
   a.tensors = mp.tensors;
   a.coef = mp.coef;
   a.stored = mp.stored;
+  a.coarse = mp.coarse;
   a.count = count;
   a.from_memory = count > MA_PTRS ? 1 : 0;
   a.m = state->m;

@@ -103,7 +103,7 @@ class MultiAdamW:
         for e, p, c in zip(table, self.params, self.copies):
             e.param, e.copy, e.n = p.data_ptr(), None if c is None else c.data_ptr(), p.numel()
         L = lib()
-        size = L.qlora_multi_adamw_plan_size(n)
+        size = L.qlora_multi_adamw_plan_size(n, self._elems)
         self._plan = torch.empty(size, dtype=torch.uint8, device=self.device)
         with torch.cuda.device(self.device):
             _check(L.qlora_multi_adamw_plan(ctypes.cast(table, ctypes.c_void_p), n,

@@ -369,8 +369,8 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
  * Zero-initialised state (scales too) is the start of training.
  *
  * qlora_multi_adamw_plan: writes the table of `count` tensors (host array) into
- *   `plan`, device memory of qlora_multi_adamw_plan_size(count) bytes, ordered on
- *   `stream`; not during stream capture (QLORA_ERR_UNSUPPORTED).  The plan also
+ *   `plan`, device memory of qlora_multi_adamw_plan_size(count, N) bytes, ordered
+ *   on `stream`; not during stream capture (QLORA_ERR_UNSUPPORTED).  The plan also
  *   holds the partial sums of a step: steps that share one plan must be ordered.
  *   param : fp32 [n], updated in place, 4-byte aligned (16 is faster);
  *   copy  : bf16 [n] or NULL, receives bf16(param);  n >= 1.
@@ -399,7 +399,7 @@ typedef struct qlora_adamw_state_t {
     int32_t  bits;
 } qlora_adamw_state_t;
 int64_t qlora_multi_adamw_state_elems(const qlora_adamw_tensor_t* tensors, int count);
-size_t qlora_multi_adamw_plan_size(int count);
+size_t qlora_multi_adamw_plan_size(int count, int64_t state_elems);
 int qlora_multi_adamw_plan(const qlora_adamw_tensor_t* tensors, int count, void* plan, size_t plan_bytes,
                            void* stream);
 int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t state_elems,

@@ -32,11 +32,12 @@ def test_state_starts_every_tensor_in_a_new_block(L):
     assert L.qlora_multi_adamw_state_elems(ctypes.cast(t, P), 3) == 256 + 256 + 512
     assert L.qlora_multi_adamw_state_elems(ctypes.cast(_table((FAKE, None, 0)), P), 1) == 0
     assert L.qlora_multi_adamw_state_elems(None, 1) == 0
-    assert L.qlora_multi_adamw_plan_size(0) == 0 and L.qlora_multi_adamw_plan_size(3) > 0
+    assert L.qlora_multi_adamw_plan_size(0, 256) == 0 and L.qlora_multi_adamw_plan_size(3, 0) == 0
+    assert L.qlora_multi_adamw_plan_size(3, 1024) > 0
 
 
 def test_plan_refusals(L):
-    size = L.qlora_multi_adamw_plan_size(1)
+    size = L.qlora_multi_adamw_plan_size(1, 256)
 
     def plan(rows, n=1, ws=FAKE, nbytes=size):
         return L.qlora_multi_adamw_plan(ctypes.cast(_table(rows), P), n, P(ws), nbytes, None)
@@ -52,7 +53,7 @@ def test_plan_refusals(L):
 
 
 def test_step_refusals(L):
-    size = L.qlora_multi_adamw_plan_size(1)
+    size = L.qlora_multi_adamw_plan_size(1, 256)
     n0 = L.qlora_launch_count()
 
     def step(g=FAKE, gd=0, bits=32, elems=256, count=1, nbytes=size, state=None, **hp):
