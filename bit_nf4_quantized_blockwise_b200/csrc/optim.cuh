@@ -303,6 +303,38 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
   }
 }
 
+// Two fp32 values in a 64-bit register and the packed operations on them.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Square root and reciprocal to 1 ulp; subnormal arguments count as 0.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // E4M3 codes of a lane's 8 values of a block under inv = 448 / max, and back.
 template <bool kRoot>
 __device__ __forceinline__ uint2 state_encode(const float (&x)[8], float inv) {
@@ -311,10 +343,11 @@ __device__ __forceinline__ uint2 state_encode(const float (&x)[8], float inv) {
   for (int h = 0; h < 2; ++h) {
     float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = __fmul_rn(x[4 * h + j], inv);
-      if (kRoot && y[j] > 0.0f && y[j] < 0x1p-9f) y[j] = 0x1p-9f;  // above 0 stays above 0
-    }
+    for (int j = 0; j < 4; j += 2) unpack2(mul2(pack2(x[4 * h + j], x[4 * h + j + 1]), dup_f32x2(inv)), y[j], y[j + 1]);
+    if (kRoot)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)  // above 0 stays above 0
+        y[j] = fmaxf(y[j], fminf(x[4 * h + j] * 0x1p100f, 0x1p-9f));
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     w[h] = lo | (hi << 16);
@@ -330,22 +363,8 @@ __device__ __forceinline__ void state_decode(uint2 w, float scale, float (&x)[8]
     for (int j = 0; j < 2; ++j) {
       const __half2 v = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(ws[h] >> (16 * j)), __NV_E4M3));
       const float2 f = __half22float2(v);
-      x[4 * h + 2 * j] = __fmul_rn(f.x, scale);
-      x[4 * h + 2 * j + 1] = __fmul_rn(f.y, scale);
+      unpack2(mul2(pack2(f.x, f.y), dup_f32x2(scale)), x[4 * h + 2 * j], x[4 * h + 2 * j + 1]);
     }
-}
-
-// Square root (subnormal arguments included: the roots of small v count) and
-// reciprocal to 1 ulp.
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 
 // The scale of a block and the factor of its codes, from the largest
@@ -389,6 +408,9 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
   if (b0 >= b1) return;
   pdl_wait();  // coefficients, and the step before this one
   const float clip = __ldcg(&a.head->clip);
+  const uint64_t clip2 = dup_f32x2(clip), one_m_b1_2 = dup_f32x2(one_m_b1), minus1_2 = dup_f32x2(-1.0f);
+  const uint64_t b2s_2 = dup_f32x2(a.beta2 * 0x1p24f), one_m_b2s_2 = dup_f32x2(one_m_b2 * 0x1p24f);
+  const uint64_t eps_2 = dup_f32x2(a.eps), decay_2 = dup_f32x2(decay);
   int t = multi_find(a, b1 - 1);
   for (int64_t top = b1; top > b0; --t) {
     const MultiTensor ts = a.tensors[t];
@@ -400,6 +422,7 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
     }
     const float step_size = __ldcg(&a.coef[t].step_size);
     const float root = __ldcg(k8 ? &a.coef[t].bc2_inv : &a.coef[t].bc2_sqrt);
+    const uint64_t root_2 = dup_f32x2(root * 0x1p-12f), minus_step_2 = dup_f32x2(-step_size);
     const bool vec = vec_ok(ts.p, 16) && vec_ok(ts.copy, 8), gvec = vec_ok(g, 4 * sizeof(G));
     auto left_of = [&](int64_t b) -> int {
       const int64_t n = ts.n - (b - ts.block0) * MA_BLOCK;
@@ -432,14 +455,23 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
       float(&p)[8] = cur.p;
       float m[8], r[8], v[8];
       if constexpr (k8) {
+        // Two elements an instruction (f32x2).  v is kept times 2^24 (its factors are), so that the
+        // root, which takes subnormal arguments as 0, loses none; r then is times 2^12.
         state_decode(cur.mw, cur.ms, m);
         state_decode(cur.vw, cur.vs, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float gi = cur.g[j] * clip;
-          m[j] = fmaf(one_m_b1, gi - m[j], m[j]);
-          r[j] = sqrt_approx(fmaf(a.beta2 * r[j], r[j], one_m_b2 * gi * gi));
-          p[j] = fmaf(p[j], decay, -step_size * (m[j] * rcp_approx(fmaf(r[j], root, a.eps))));
+        for (int j = 0; j < 8; j += 2) {
+          const uint64_t g2 = mul2(pack2(cur.g[j], cur.g[j + 1]), clip2), m0 = pack2(m[j], m[j + 1]);
+          const uint64_t m2 = fma2(one_m_b1_2, fma2(m0, minus1_2, g2), m0);
+          const uint64_t r0 = pack2(r[j], r[j + 1]);
+          const uint64_t v2 = fma2(mul2(b2s_2, r0), r0, mul2(mul2(one_m_b2s_2, g2), g2));
+          unpack2(v2, r[j], r[j + 1]);
+          r[j] = sqrt_approx(r[j]), r[j + 1] = sqrt_approx(r[j + 1]);
+          float d0, d1;
+          unpack2(fma2(pack2(r[j], r[j + 1]), root_2, eps_2), d0, d1);
+          const uint64_t q2 = mul2(m2, pack2(rcp_approx(d0), rcp_approx(d1)));
+          unpack2(fma2(q2, minus_step_2, mul2(pack2(p[j], p[j + 1]), decay_2)), p[j], p[j + 1]);
+          unpack2(m2, m[j], m[j + 1]);
         }
         if (left < MA_BLOCK) {  // what lies behind the tensor's end does not count for the block
 #pragma unroll
@@ -480,7 +512,8 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
         }
         float ms, minv, rs, rinv;
         block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mtop)), ms, minv);
-        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rtop)), rs, rinv);
+        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rtop * 0x1p-12f)), rs, rinv);
+        rinv *= 0x1p-12f;  // r is times 2^12
         const uint2 mw = state_encode<false>(m, minv), vw = state_encode<true>(r, rinv);
         uint32_t* mc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + b * MA_BLOCK) + lane;
         uint32_t* vc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + b * MA_BLOCK) + lane;
