@@ -115,6 +115,10 @@ constexpr int MA_COARSE = 64;
 // warps: 8 bits 722 / 705 / 751 us a step of 160 M parameters at 2 / 3 / 4 CTAs,
 // 32 bits 895 / 984 at 2 / 3.
 constexpr int MA_PER_SM8 = 3, MA_PER_SM32 = 2;
+// CTAs that take the blocks of one contiguous range in turn.  Fewer ranges mean fewer places of the
+// seven arrays being read and written at a time: 8 bits 677 us with a range each, 632 with three
+// CTAs a range (640 and 634 with 12 and 37); 32 bits 870 and, with two, 865.
+constexpr int MA_SHARE8 = 3, MA_SHARE32 = 2;
 constexpr int MA_PTRS = 496;          // gradient pointers passed with a launch (under 4 KB of parameters)
 constexpr int MA_NORM_CTAS = 148 * 4; // partial sums of the norm, one per CTA
 constexpr int MA_UNROLL = 4;          // blocks of gradients a warp loads at a time for the norm
@@ -155,6 +159,7 @@ struct MultiAdamWParams {
   int32_t* steps;         // [count] completed steps of each tensor
   float lr, beta1, beta2, eps, weight_decay, max_grad_norm;
   int clip;               // clip by the global norm
+  int share;              // CTAs that take the blocks of one contiguous range in turn
 };
 
 struct GradPtrs {
@@ -249,7 +254,9 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
   double s = 0.0;
   if (a.clip) {
     const int64_t blocks = a.head->blocks;
-    const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+    const int ranges = gridDim.x / a.share, range = blockIdx.x % ranges;
+    const int mine = static_cast<int>(blockIdx.x / ranges) * MA_WARPS + warp, step = a.share * MA_WARPS;
+    const int64_t b0 = blocks * range / ranges, b1 = blocks * (range + 1) / ranges;
     int t = b0 < b1 ? multi_find(a, b0) : 0;
     for (int64_t b = b0; b < b1; ++t) {
       const MultiTensor ts = a.tensors[t];
@@ -259,12 +266,12 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
       if (g) {
         const bool vec = vec_ok(g, 4 * sizeof(G));
         // four blocks a warp at a time: 4 KB of loads in flight
-        for (int64_t k = b + warp; k < end; k += MA_UNROLL * MA_WARPS) {
+        for (int64_t k = b + mine; k < end; k += MA_UNROLL * step) {
           float x[MA_UNROLL][8];
 #pragma unroll
           for (int u = 0; u < MA_UNROLL; ++u) {
-            const int64_t e = (k + u * MA_WARPS - ts.block0) * MA_BLOCK;
-            const int64_t left = k + u * MA_WARPS < end ? ts.n - e : 0;
+            const int64_t e = (k + u * step - ts.block0) * MA_BLOCK;
+            const int64_t left = k + u * step < end ? ts.n - e : 0;
             load8<G>(g + e, static_cast<int>(left < MA_BLOCK ? left : MA_BLOCK), vec, lane, x[u]);
           }
 #pragma unroll
@@ -387,22 +394,26 @@ struct MultiLoads {
   float ms, vs;
 };
 
-// The update.  Every CTA has a contiguous range of blocks, which its warps take
-// in turn from the end to the beginning: the norm read the range upwards, so
-// the gradients it read last are still in L2.  A warp loads its next block of
-// the tensor before it computes the present one.
+// The update.  The blocks of a contiguous range are taken in turn by the warps of
+// the CTAs that share it, from the end to the beginning: the norm read the range
+// upwards, so the gradients it read last are still in L2.  A warp loads its next
+// block of the tensor before it computes the present one.
 //   32 bits: adamw_kernel's order and rounding (fp32 IEEE throughout), so the
 //   result is that of qlora_adamw_step bit for bit; bound by DRAM.
 //   8 bits: with IEEE square roots and divisions the kernel is bound by
-//   instruction issue, not by DRAM (a step over 160 M parameters: 990 us, with
-//   the approximate root, reciprocal and fused multiply-adds below 705 us); they
-//   cost 4 ulp of the update, far below p's own rounding.
+//   instruction issue, not by DRAM (a step over 160 M parameters: 990 us; with
+//   the approximate root, reciprocal and packed fused multiply-adds below 632 us,
+//   3.5 GB at 5.6 TB/s); they cost 4 ulp of the update, far below p's own
+//   rounding.  A ring of three or four blocks a warp in shared memory, filled by
+//   cp.async, was slower (716 to 802 us for 684 then).
 template <bool k8, typename G>
 __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
     multi_adamw_kernel(const __grid_constant__ MultiAdamWParams a, const __grid_constant__ GradPtrs gp) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t blocks = a.head->blocks;
-  const int64_t b0 = blocks * blockIdx.x / gridDim.x, b1 = blocks * (blockIdx.x + 1) / gridDim.x;
+  const int ranges = gridDim.x / a.share, range = blockIdx.x % ranges;
+  const int mine = static_cast<int>(blockIdx.x / ranges) * MA_WARPS + warp, step = a.share * MA_WARPS;
+  const int64_t b0 = blocks * range / ranges, b1 = blocks * (range + 1) / ranges;
   const float decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
   const float one_m_b1 = __fsub_rn(1.0f, a.beta1), one_m_b2 = __fsub_rn(1.0f, a.beta2);
   if (b0 >= b1) return;
@@ -445,11 +456,11 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
         load8<float>(static_cast<const float*>(a.v) + b * MA_BLOCK, MA_BLOCK, true, lane, x.v);
       }
     };
-    int64_t b = top - 1 - warp;
+    int64_t b = top - 1 - mine;
     MultiLoads<k8> cur, nxt;
     if (b >= lo) load(b, cur);
-    for (; b >= lo; b -= MA_WARPS) {
-      if (b - MA_WARPS >= lo) load(b - MA_WARPS, nxt);
+    for (; b >= lo; b -= step) {
+      if (b - step >= lo) load(b - step, nxt);
       const int64_t e = (b - ts.block0) * MA_BLOCK;
       const int left = left_of(b);
       float(&p)[8] = cur.p;

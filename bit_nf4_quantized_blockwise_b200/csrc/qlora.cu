@@ -1223,11 +1223,12 @@ MultiPlan multi_plan_layout(void* base, int count, int64_t blocks) {
 constexpr int kMaxTensors = 1 << 20;
 
 template <bool k8, typename G>
-int launch_multi_adamw(const MultiAdamWParams& a, const GradPtrs& gp, int64_t blocks, cudaStream_t st) {
+int launch_multi_adamw(MultiAdamWParams a, const GradPtrs& gp, int64_t blocks, cudaStream_t st) {
   const int64_t ctas = (blocks + MA_WARPS - 1) / MA_WARPS;
   const int64_t most = static_cast<int64_t>(sm_count()) * (k8 ? MA_PER_SM8 : MA_PER_SM32);
   int64_t grid = ctas < most ? ctas : most;
   if (grid > MA_NORM_CTAS) grid = MA_NORM_CTAS;
+  a.share = grid == most ? (k8 ? MA_SHARE8 : MA_SHARE32) : 1;
   const int64_t norm = a.clip ? grid : 1;  // the update's ranges: see multi_adamw_kernel
   {
     LaunchScope ls(QLORA_KERNEL_OPTIM, st);
