@@ -1899,6 +1899,13 @@ int launch_multi_grad(const void* X, const void* dY, const MultiWs& w, const qlo
                           MD_THREADS, MD_SMEM, st, mx, mxs, md, mds, mu, mt, p, v);
 }
 
+// Sizes that the layer takes; a workspace query for others answers 0.
+bool multi_sizes_ok(int64_t o, int64_t h, int64_t M, int n, int r) {
+  const int64_t most = int64_t(1) << 30;
+  return o >= 64 && h >= 64 && o % 64 == 0 && h % 64 == 0 && o <= most && h <= most && r >= 8 &&
+         r <= QLORA_MAX_RANK && r % 8 == 0 && check_plan_args(M, n) == QLORA_OK;
+}
+
 int check_multi_args(const qlora_nf4_t* Wq, int64_t M, const qlora_adapters_t* ad, int dtype, const void* plan,
                      size_t plan_bytes) {
   if (!ad) return QLORA_ERR_NULL;
@@ -1937,11 +1944,11 @@ int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, siz
 }
 
 size_t qlora_multi_linear_fwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r) {
-  return multi_ws_layout(nullptr, o, h, M, n, r, false).bytes;
+  return multi_sizes_ok(o, h, M, n, r) ? multi_ws_layout(nullptr, o, h, M, n, r, false).bytes : 0;
 }
 
 size_t qlora_multi_linear_bwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r) {
-  return multi_ws_layout(nullptr, o, h, M, n, r, true).bytes;
+  return multi_sizes_ok(o, h, M, n, r) ? multi_ws_layout(nullptr, o, h, M, n, r, true).bytes : 0;
 }
 
 int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, const qlora_adapters_t* ad,

@@ -46,6 +46,15 @@ def test_plan_refusals(L):
     assert L.qlora_launch_count() == n0
 
 
+@pytest.mark.parametrize("bad", [
+    (O, H, 64, 0, R), (O, H, 0, N, R), (O, H, 0, 0, R), (O, H, -1, N, R), (O, H, (1 << 28) + 1, N, R),
+    (O, H, M, 65536, R), (O, H, M, N, 0), (O, H, M, N, 12), (O, H, M, N, 264), (O, H, M, N, -8),
+    (0, H, M, N, R), (O, 0, M, N, R), (O, 32, M, N, R), (96, H, M, N, R), (-64, H, M, N, R), (O, 1 << 31, M, N, R)])
+def test_workspace_query_of_sizes_that_are_not_taken(L, bad):
+    assert L.qlora_multi_linear_fwd_workspace_size(*bad) == 0
+    assert L.qlora_multi_linear_bwd_workspace_size(*bad) == 0
+
+
 def test_layer_refusals(L):
     plan = L.qlora_adapter_plan_size(M, N)
     wf = L.qlora_multi_linear_fwd_workspace_size(O, H, M, N, R)
