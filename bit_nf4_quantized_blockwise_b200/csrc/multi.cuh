@@ -719,6 +719,16 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float x) {
   return x;
 }
 
+// x += a w for eight columns.
+__device__ __forceinline__ void axpy8(float a, uint4 w, float (&x)[8]) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    x[2 * c] = fmaf(a, __uint_as_float(ws[c] << 16), x[2 * c]);
+    x[2 * c + 1] = fmaf(a, __uint_as_float(ws[c] & 0xFFFF0000u), x[2 * c + 1]);
+  }
+}
+
 // The slot row of sorted row m, or null for a row without adapter, and its adapter.
 __device__ __forceinline__ const uint16_t* slot_row(const MultiPairParams& p, const PlanView& v, int m, int& adapter) {
   const int t = m / MP_SLOT_ROWS;
@@ -731,28 +741,40 @@ __device__ __forceinline__ const uint16_t* slot_row(const MultiPairParams& p, co
   return nullptr;
 }
 
-// One element from its own row and adapter alone, in fp32.
+// Eight elements n .. n + 7 from their own row and adapter alone, in fp32.
 template <bool kBwd>
-__device__ float multi_element(const MultiPairParams& p, const uint16_t* a, const uint16_t* row, int adapter, int n) {
-  float x = 0.0f;
-  if (kBwd) {
-    for (int k = 0; k < p.K; ++k)
-      x = fmaf(bf16_bits_to_float(a[k]), bf16_bits_to_float(p.Wd[static_cast<int64_t>(k) * p.g.N + n]), x);
-  } else {
-    const uint16_t* w = p.Wd + static_cast<int64_t>(n) * p.K;
-    for (int k = 0; k < p.K; k += 8)  // K is a multiple of 64
-      x = dot8(*reinterpret_cast<const uint4*>(a + k), *reinterpret_cast<const uint4*>(w + k), x);
-  }
-  if (row) {
-    const uint16_t* b = p.bank + static_cast<int64_t>(adapter) * p.r * p.g.N;
-    float d = 0.0f;
-    for (int j = 0; j < p.r; ++j) {
-      const float w = bf16_bits_to_float(b[kBwd ? static_cast<int64_t>(n) * p.r + j : static_cast<int64_t>(j) * p.g.N + n]);
-      d = fmaf(bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]), w, d);
+__device__ __forceinline__ void multi_elements(const MultiPairParams& p, const uint16_t* a, const uint16_t* row,
+                                               int adapter, int n, float (&x)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) x[c] = 0.0f;
+  for (int k = 0; k < p.K; k += 8) {  // K is a multiple of 64
+    const uint4 av = *reinterpret_cast<const uint4*>(a + k);
+    if (kBwd) {
+      const uint32_t as[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        axpy8(__uint_as_float(i & 1 ? as[i / 2] & 0xFFFF0000u : as[i / 2] << 16),
+              *reinterpret_cast<const uint4*>(p.Wd + static_cast<int64_t>(k + i) * p.g.N + n), x);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        x[c] = dot8(av, *reinterpret_cast<const uint4*>(p.Wd + static_cast<int64_t>(n + c) * p.K + k), x[c]);
     }
-    x += d;
   }
-  return x;
+  if (!row) return;
+  const uint16_t* b = p.bank + static_cast<int64_t>(adapter) * p.r * p.g.N;
+  float d[8] = {};
+  for (int j = 0; j < p.r; ++j) {
+    const float t = bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]);
+    if (kBwd) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) d[c] = fmaf(t, bf16_bits_to_float(b[static_cast<int64_t>(n + c) * p.r + j]), d[c]);
+    } else {
+      axpy8(t, *reinterpret_cast<const uint4*>(b + static_cast<int64_t>(j) * p.g.N + n), d);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) x[c] += d[c];
 }
 
 // Whether rows of several owners (groups, or none) meet in a 256-row tile.
@@ -772,11 +794,12 @@ __device__ __forceinline__ bool all_finite(const float* x) {
   return z == 0.0f;
 }
 
-// Replaces what is not finite among the `len` elements from n on that this thread has stored of
-// sorted row m by its own sum; nothing to do where the row itself is not finite, or its product with
-// its adapter's first factor is NaN (then all its elements are).  So a batch of NaN costs a look at
-// its rows, and one adapter of NaN the tiles it shares with others (a few milliseconds a tile).
-// Never inlined: the path is rare and long.
+// Replaces what is not finite among the `len` elements (a multiple of 8) from n on that this thread
+// has stored of sorted row m by its own sum; nothing to do where the row itself is not finite, or its
+// product with its adapter's first factor is NaN (then all its elements are).  So a batch of NaN costs
+// a look at its rows, and one adapter of infinities, or sums that overflow, 12 to 20 ms at 4096 x 4096 x
+// 11008 (eight elements at a time, so that each load of the row and of W' serves eight).  Never
+// inlined: the path is rare and long.
 template <bool kBwd>
 __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, int len) {
   const uint16_t* a = p.A + static_cast<int64_t>(v.perm[m]) * p.K;
@@ -793,14 +816,22 @@ __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanVi
       if ((w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u) return;
   }
   const int64_t at = static_cast<int64_t>(v.perm[m]) * p.g.ld_out + n;
-  for (int t = 0; t < len; ++t) {
-    if (p.g.out_bf16) {
-      uint16_t* o = static_cast<uint16_t*>(p.g.out) + at + t;
-      if (!isfinite(bf16_bits_to_float(*o)))
-        *o = __bfloat16_as_ushort(__float2bfloat16_rn(multi_element<kBwd>(p, a, row, adapter, n + t)));
-    } else {
-      float* o = static_cast<float*>(p.g.out) + at + t;
-      if (!isfinite(*o)) *o = multi_element<kBwd>(p, a, row, adapter, n + t);
+  uint16_t* o16 = static_cast<uint16_t*>(p.g.out) + at;
+  float* o32 = static_cast<float*>(p.g.out) + at;
+  for (int t = 0; t < len; t += 8) {
+    unsigned bad = 0;
+    for (int c = 0; c < 8; ++c)
+      if (!isfinite(p.g.out_bf16 ? bf16_bits_to_float(o16[t + c]) : o32[t + c])) bad |= 1u << c;
+    if (bad == 0) continue;
+    float x[8];
+    multi_elements<kBwd>(p, a, row, adapter, n + t, x);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (!(bad >> c & 1)) continue;
+      if (p.g.out_bf16)
+        o16[t + c] = __bfloat16_as_ushort(__float2bfloat16_rn(x[c]));
+      else
+        o32[t + c] = x[c];
     }
   }
 }
@@ -808,10 +839,10 @@ __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanVi
 // Fewer tiles than SM pairs (`even`): the K stages of all tiles, one tile after
 // the other, are dealt out in equal contiguous shares, so that every pair works
 // for the same time whatever the number of tiles and of slots in them (333
-// tokens, 13824 x 5120: 40 tiles on 74 pairs, 99 us with one tile a pair,
-// EVEN333).  A share's first and last tile may be partial: their sums go to
-// the pair's two places of the partial buffer, and multi_reduce_kernel adds
-// the places of a tile in order.
+// tokens, 13824 x 5120, 40 tiles on 74 pairs: the call takes 165 us with one tile
+// a pair, 130 so).  A share's first and last tile may be partial: their sums go to
+// the pair's two places of the partial buffer, and multi_reduce_kernel adds the
+// places of a tile in order.
 struct StageShare {
   int64_t lo, hi;  // stages of this pair
 };
@@ -1298,18 +1329,37 @@ struct MultiGradParams {
   unsigned* counters;  // [group][tile], zero at launch
 };
 
-// One element of a factor's gradient from the group's own tokens alone, in fp32.
-__device__ __noinline__ float grad_element(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j) {
+// Replaces what is not finite among the `ranks` elements (a multiple of 8) of row m of a factor's
+// gradient, from rank j0 on, that this thread has stored at out (`ld` apart) by the sum over the group's
+// own tokens, in fp32, eight ranks at a time.  Never inlined: the path is rare and long.
+__device__ __noinline__ void grad_repair(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j0,
+                                         int ranks, float* out, int64_t ld) {
   const PlanGroup pg = plan_load(v.groups + grp);
-  float y = 0.0f;
-  for (int row = pg.start; row < pg.end; ++row) {
-    const int64_t slot_row =
-        static_cast<int64_t>(pg.slot0 + row / MP_SLOT_ROWS - pg.start / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
-    const uint16_t* b = side.slots + slot_row * (MD_PARTS * rp) + j;
-    const float w = bf16_bits_to_float(b[0]) + bf16_bits_to_float(b[rp]) + bf16_bits_to_float(b[2 * rp]);
-    y = fmaf(bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]), w, y);
+  const int64_t slot0 = pg.slot0 - pg.start / MP_SLOT_ROWS;
+  for (int t = 0; t < ranks; t += 8) {
+    unsigned bad = 0;
+    for (int c = 0; c < 8; ++c)
+      if (!isfinite(out[(t + c) * ld])) bad |= 1u << c;
+    if (bad == 0) continue;
+    float x[8] = {};
+#pragma unroll 4
+    for (int row = pg.start; row < pg.end; ++row) {
+      const int64_t slot_row = (slot0 + row / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
+      const uint16_t* b = side.slots + slot_row * (MD_PARTS * rp) + j0 + t;
+      const uint4 hi = *reinterpret_cast<const uint4*>(b), mid = *reinterpret_cast<const uint4*>(b + rp),
+                  lo = *reinterpret_cast<const uint4*>(b + 2 * rp);
+      float w[8] = {};  // the sum of the parts
+      axpy8(1.0f, hi, w);
+      axpy8(1.0f, mid, w);
+      axpy8(1.0f, lo, w);
+      const float a = bf16_bits_to_float(side.A[static_cast<int64_t>(v.perm[row]) * side.rows + m]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) x[c] = fmaf(a, w[c], x[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (bad >> c & 1) out[(t + c) * ld] = x[c];
   }
-  return y;
 }
 
 __global__ void __launch_bounds__(MD_THREADS, 1)
@@ -1499,22 +1549,6 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
       }
       const int m = it.m0 + row;
       if (m >= side.rows) continue;
-      // rows of others in the group's first or last block
-      if (it.grp >= 0 && (it.pg.start % MD_BK != 0 || (it.pg.end % MD_BK != 0 && it.pg.end < v.M))) {
-        float z = 0.0f;
-#pragma unroll
-        for (int j = 0; j < MD_BN; ++j) z = fmaf(x[j], 0.0f, z);
-        if (z != 0.0f)
-          for (int t = 0; t < MD_BN && it.j0 + t < p.r; ++t) {
-            float y = 0.0f;
-#pragma unroll
-            for (int j = 0; j < MD_BN; ++j) y = j == t ? x[j] : y;
-            if (isfinite(y)) continue;
-            y = grad_element(side, v, it.grp, p.rp, m, it.j0 + t);
-#pragma unroll
-            for (int j = 0; j < MD_BN; ++j) x[j] = j == t ? y : x[j];
-          }
-      }
       float* out = side.out + static_cast<int64_t>(it.adapter) * p.r * side.rows;
       const int ranks = min(MD_BN, p.r - it.j0);
       if (it.second) {
@@ -1526,6 +1560,14 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < MD_BN; j += 4)
           if (j < ranks) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      }
+      // rows of others in the group's first or last block
+      if (it.grp >= 0 && (it.pg.start % MD_BK != 0 || (it.pg.end % MD_BK != 0 && it.pg.end < v.M)) &&
+          !all_finite<MD_BN>(x)) {
+        if (it.second)
+          grad_repair(side, v, it.grp, p.rp, m, it.j0, ranks, out + static_cast<int64_t>(it.j0) * side.rows + m, side.rows);
+        else
+          grad_repair(side, v, it.grp, p.rp, m, it.j0, ranks, out + static_cast<int64_t>(m) * p.r + it.j0, 1);
       }
     }
   }
