@@ -342,6 +342,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+// The larger of two values, NaN where one of them is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 // E4M3 codes of a lane's 8 values of a block under inv = 448 / max, and back.
 template <bool kRoot>
 __device__ __forceinline__ uint2 state_encode(const float (&x)[8], float inv) {
@@ -354,7 +361,7 @@ __device__ __forceinline__ uint2 state_encode(const float (&x)[8], float inv) {
     if (kRoot)
 #pragma unroll
       for (int j = 0; j < 4; ++j)  // above 0 stays above 0
-        y[j] = fmaxf(y[j], fminf(x[4 * h + j] * 0x1p100f, 0x1p-9f));
+        y[j] = max_nan(y[j], fminf(x[4 * h + j] * 0x1p100f, 0x1p-9f));
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
     w[h] = lo | (hi << 16);
@@ -377,7 +384,7 @@ __device__ __forceinline__ void state_decode(uint2 w, float scale, float (&x)[8]
 // The scale of a block and the factor of its codes, from the largest
 // magnitude's bits.  Blocks below 2^-100 (448 / max would overflow) hold zeros.
 // A NaN does not count (it has a code of its own); an infinity makes the scale
-// infinite, and its block decodes to NaN.
+// infinite, and the block decodes to NaN (roots above 0 that are finite to infinity).
 __device__ __forceinline__ void block_scale(uint32_t top_bits, float& scale, float& inv) {
   const float top = __uint_as_float(top_bits);
   const bool dead = top < 0x1p-100f;

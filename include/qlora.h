@@ -380,8 +380,9 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
  *           and its step count as they are.  Not modified.
  *   hp    : step is not used (see steps); max_grad_norm <= 0: no clipping.
  *   A gradient with NaN or infinity: the norm clips nothing (NaN) or everything
- *   (infinity), as in qlora_adamw_step; its element becomes NaN, and with
- *   8-bit state an infinity makes its whole block of state NaN.
+ *   (infinity), as in qlora_adamw_step; its element becomes NaN.  With 8-bit
+ *   state a NaN's m and r are NaN too, and an infinity makes m of its whole
+ *   block NaN and r NaN or infinite, so that the next step's result is NaN there.
  * With 32-bit state the results are those of qlora_adamw_step bit for bit; with
  * 8-bit state the root and the quotient of the update are good to 4 ulp.     */
 #define QLORA_STATE_BLOCK 256

@@ -261,6 +261,18 @@ def test_nonfinite_gradient_stays_in_its_element_or_block(bits, value):
     assert bad == (list(range(256, 512)) if bits == 8 and value == float("inf") else [300])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_moments_of_a_nan_gradient_are_nan(bits):
+    opt = MultiAdamW(_tensors([(1024,)]), AdamWConfig(lr=1e-3, max_grad_norm=None), state_bits=bits)
+    g = _grads([(1024,)], 1)
+    g[0][300] = float("nan")
+    for t in (2, 3):
+        opt.step(g)
+        for x in opt.moments(0):
+            assert torch.isnan(x).nonzero().view(-1).tolist() == [300]
+        g = _grads([(1024,)], t)
+
+
 def test_state_moves_between_optimizers():
     a = MultiAdamW(_tensors(SHAPES), CFG, state_bits=8)
     for t in (1, 2):
