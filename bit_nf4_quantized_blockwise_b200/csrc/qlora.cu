@@ -236,6 +236,18 @@ int set_smem(K kernel, int bytes) {
              : QLORA_ERR_CUDA;
 }
 
+// set_smem with the same bytes at every call of a kernel, done once per device.
+template <auto kKernel>
+int set_smem_once(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return QLORA_OK;
+  if (set_smem(kKernel, bytes) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
+  return QLORA_OK;
+}
+
 int check_wq(const qlora_nf4_t* Wq) {
   if (!Wq) return QLORA_ERR_NULL;
   if (!Wq->codes) return QLORA_ERR_NULL;
@@ -396,7 +408,7 @@ int dequant_into(const qlora_nf4_t* Wq, uint16_t* out, int family, cudaStream_t 
   p.nwords = Wq->o * Wq->h / 8;
   p.nblocks = Wq->o * Wq->h / 64;
   std::memcpy(p.codebook, Wq->codebook, sizeof(p.codebook));
-  if (set_smem(nf4_dequant_kernel, kDequantSmem) != QLORA_OK) return QLORA_ERR_CUDA;
+  if (set_smem_once<nf4_dequant_kernel>(kDequantSmem) != QLORA_OK) return QLORA_ERR_CUDA;
   const int64_t grid = grid_for(p.nwords, kDequantThreads * kDequantWords, sm_count());
   {
     LaunchScope ls(family, st);
@@ -1596,18 +1608,6 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   return w;
 }
 
-// set_smem with the same bytes at every call of a kernel, done once per device.
-template <auto kKernel>
-int set_smem_once(int bytes) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return QLORA_ERR_CUDA;
-  if (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)) return QLORA_OK;
-  if (set_smem(kKernel, bytes) != QLORA_OK) return QLORA_ERR_CUDA;
-  if (dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
-  return QLORA_OK;
-}
-
 // A kernel as the programmatic dependent of the one before it on the stream.
 template <typename K, typename... Args>
 int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
@@ -1635,9 +1635,9 @@ int sort_rows(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_
   p.src[1] = static_cast<const uint4*>(D);
   p.dst[1] = reinterpret_cast<uint4*>(Ds);
   p.vecs[1] = static_cast<int>(d_width / 8);
-  const int64_t most = static_cast<int64_t>(v.M) * (width > d_width ? width : d_width) / 8;
-  const dim3 grid(static_cast<unsigned>(grid_for(most, 1024, sm_count() * 8)), D ? 2 : 1);
-  return launch_dependent(multi_sort_rows_kernel, grid, 256, 0, st, p, v);
+  const int64_t most = MC_PER_SM * sm_count();
+  const dim3 grid(static_cast<unsigned>(v.M < most ? v.M : most));
+  return launch_dependent(multi_sort_rows_kernel, grid, MC_THREADS, 0, st, p, v);
 }
 
 template <int RP, bool kKN>
@@ -1820,7 +1820,9 @@ int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapte
     dp.out = acc;
     std::memcpy(dp.codebook, Wq->codebook, sizeof(dp.codebook));
     auto kernel = M <= 8 ? small_m_mma_kernel<1, false> : small_m_mma_kernel<2, false>;
-    if (set_smem(kernel, SD_SMEM_BYTES) != QLORA_OK) return QLORA_ERR_CUDA;
+    if ((M <= 8 ? set_smem_once<small_m_mma_kernel<1, false>>(SD_SMEM_BYTES)
+                : set_smem_once<small_m_mma_kernel<2, false>>(SD_SMEM_BYTES)) != QLORA_OK)
+      return QLORA_ERR_CUDA;
     LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
     rc = launch_dependent(kernel, dim3(static_cast<unsigned>(dp.units < sm_count() ? dp.units : sm_count())), SD_THREADS,
                           SD_SMEM_BYTES, st, mc, mx, dp);
