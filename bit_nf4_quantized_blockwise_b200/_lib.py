@@ -293,18 +293,11 @@ class NF4Weight:
         return self.absmax is None
 
     def struct(self) -> qlora_nf4_t:
-        s = qlora_nf4_t()
-        s.codes = self.codes.data_ptr()
-        s.absmax_fp8 = self.absmax_fp8.data_ptr() if self.absmax_fp8 is not None else None
-        s.dq_scale = self.dq_scale.data_ptr() if self.dq_scale is not None else None
-        s.dq_mean = self.dq_mean.data_ptr() if self.dq_mean is not None else None
-        s.o = self.o
-        s.h = self.h
-        s.codebook = _codebook_of(self.codebook) if type(self.codebook) is tuple else _codebook_array(self.codebook)
-        s.block = 64
-        s.dq_block = 256
-        s.absmax = self.absmax.data_ptr() if self.absmax is not None else None
-        return s
+        fp8, scale, mean, absmax, codebook = self.absmax_fp8, self.dq_scale, self.dq_mean, self.absmax, self.codebook
+        return qlora_nf4_t(self.codes.data_ptr(), None if fp8 is None else fp8.data_ptr(),
+                           None if scale is None else scale.data_ptr(), None if mean is None else mean.data_ptr(),
+                           self.o, self.h, _codebook_of(codebook) if type(codebook) is tuple else
+                           _codebook_array(codebook), 64, 256, None if absmax is None else absmax.data_ptr())
 
 
 # ---------------------------------------------------------------- entry points
@@ -608,6 +601,12 @@ def _workspace(ws: Optional[torch.Tensor], size: int, dev: torch.device) -> torc
     return ws
 
 
+@functools.lru_cache(maxsize=4096)
+def _multi_ws_size(bwd: bool, *sizes: int) -> int:
+    L = lib()
+    return (L.qlora_multi_linear_bwd_workspace_size if bwd else L.qlora_multi_linear_fwd_workspace_size)(*sizes)
+
+
 def _or_null(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -626,7 +625,7 @@ def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, pl
     if T_save is None and save_T:
         T_save = torch.empty(M, r, dtype=torch.float32, device=dev)
     L = lib()
-    ws = _workspace(ws, L.qlora_multi_linear_fwd_workspace_size(Wq.o, Wq.h, M, n, r), dev)
+    ws = _workspace(ws, _multi_ws_size(False, Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_fwd, "qlora_multi_linear_fwd", dev, Wq.struct(), X.data_ptr(), M, bank.struct(),
           plan.buffer.data_ptr(), plan.buffer.numel(), Y.data_ptr(), _dtype_code(Y.dtype), _or_null(T_save),
           ws.data_ptr(), ws.numel() * ws.element_size())
@@ -649,7 +648,7 @@ def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, ban
     if dL2 is None:
         dL2 = torch.empty(n, r, Wq.o, dtype=torch.float32, device=dev)
     L = lib()
-    ws = _workspace(ws, L.qlora_multi_linear_bwd_workspace_size(Wq.o, Wq.h, M, n, r), dev)
+    ws = _workspace(ws, _multi_ws_size(True, Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_bwd, "qlora_multi_linear_bwd", dev, Wq.struct(), X.data_ptr(), dY.data_ptr(), M,
           bank.struct(), plan.buffer.data_ptr(), plan.buffer.numel(), _or_null(T_saved), dX.data_ptr(),
           _dtype_code(dX.dtype), dL1.data_ptr(), dL2.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())

@@ -236,45 +236,6 @@ __global__ void __launch_bounds__(MP_THREADS) adapter_plan_kernel(const int* __r
   if (threadIdx.x == 0) *v.head = {groups, moved ? 0 : 1, carry.x, carry.y};
 }
 
-// Rows of X and dY in sorted order, for batches that are not in it already.  A block a row at a time,
-// eight loads a thread in flight; few enough blocks that the rank-r product, which gathers its
-// own rows, runs beside it (a call with 8190 shuffled tokens, 5120 x 13824: 1120 / 1075 / 1054 / 1054 us at
-// 1 / 2 / 4 / 8 blocks an SM).
-constexpr int MC_PER_SM = 4;
-constexpr int MC_THREADS = 256;
-struct SortParams {
-  const uint4* src[2];
-  uint4* dst[2];
-  int vecs[2];  // 16-byte vectors of a row (0: none)
-};
-__global__ void __launch_bounds__(MC_THREADS) multi_sort_rows_kernel(const SortParams p, const PlanView v) {
-  pdl_launch_dependents();
-  if (!__ldg(&v.head->in_order)) {
-    const int all = p.vecs[0] + p.vecs[1];
-    for (int64_t at = blockIdx.x; at < v.M; at += gridDim.x) {
-      const int64_t from = __ldg(v.perm + at);
-      const uint4* s0 = p.src[0] + from * p.vecs[0];
-      const uint4* s1 = p.src[1] + (from * p.vecs[1] - p.vecs[0]);
-      uint4* d0 = p.dst[0] + at * p.vecs[0];
-      uint4* d1 = p.dst[1] + (at * p.vecs[1] - p.vecs[0]);
-      for (int c0 = threadIdx.x; c0 < all; c0 += 8 * MC_THREADS) {
-        uint4 x[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int c = c0 + u * MC_THREADS;
-          if (c < all) x[u] = __ldg((c < p.vecs[0] ? s0 : s1) + c);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int c = c0 + u * MC_THREADS;
-          if (c < all) (c < p.vecs[0] ? d0 : d1)[c] = x[u];
-        }
-      }
-    }
-  }
-  pdl_wait();
-}
-
 // ====================================================================== rank-r products of the groups
 
 // D[p][j] = sum_k A[perm[p]][k] B[a][..] for 64 rows of one group and one part of
@@ -310,6 +271,18 @@ constexpr int ms_stages() {
   return RP <= 64 ? 4 : 3;
 }
 
+// Sorted copies of the rows of X (and dY), for batches that are not in the groups' order: further
+// blocks of the rank-r product's grid, which gathers its own rows and is bound by latency.  As a kernel
+// before it they were one launch more for every batch, and took 1084 us a call for 1065 (8190 shuffled
+// tokens, 5120 x 13824, backward); copied by the blocks' threads instead of bulk copies 1107.
+constexpr int MC_PER_SM = 2;  // such blocks
+struct SortParams {
+  const uint4* src[2];
+  uint4* dst[2];
+  int vecs[2];  // 16-byte vectors of a row (0: none)
+  int blocks;   // of each split
+};
+
 struct ShrinkParams {
   const uint16_t* A;   // [M][K]
   const uint16_t* B;   // bank
@@ -320,7 +293,68 @@ struct ShrinkParams {
   float* P;            // [splits][M][r]
   float* zero;         // also zeroed by the grid: the accumulator of the decode kernel, or null
   int64_t zero_len;    // a multiple of 4
+  SortParams sort;
 };
+
+// Block `block` of `blocks` copies rows through a ring of bulk copies, by one thread.
+constexpr int MC_SLOTS = 4;
+constexpr int MC_BYTES = 10240;  // of a slot; the ring fits the shared memory of every rank
+__device__ __forceinline__ void sort_rows(const SortParams& p, const PlanView& v, int block, int blocks, uint8_t* ring) {
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + MC_SLOTS * MC_BYTES);
+  for (int s = 0; s < MC_SLOTS; ++s) mbar_init(&full[s], 1);
+  fence_mbar_init();
+  struct Piece {  // the next piece to load, or to store
+    int64_t at;
+    int side, off;
+  };
+  auto bytes = [&](int side) { return 16 * (side ? p.vecs[1] : p.vecs[0]); };
+  auto src = [&](int side) { return reinterpret_cast<const uint8_t*>(side ? p.src[1] : p.src[0]); };
+  auto dst = [&](int side) { return reinterpret_cast<uint8_t*>(side ? p.dst[1] : p.dst[0]); };
+  auto next = [&](Piece& x) {
+    x.off += MC_BYTES;
+    if (x.off < bytes(x.side)) return;
+    x.off = 0;
+    if (x.side == 0 && bytes(1) > 0) {
+      x.side = 1;
+    } else {
+      x.side = 0;
+      x.at += blocks;
+    }
+  };
+  Piece in{block, 0, 0}, out = in;
+  int n_in = 0, n_out = 0;
+  int64_t from = block < v.M ? __ldg(v.perm + block) : 0, ahead = block + blocks < v.M ? __ldg(v.perm + block + blocks) : 0;
+  auto load = [&]() {
+    if (in.at >= v.M) return;
+    const int s = n_in++ % MC_SLOTS;
+    const uint32_t len = static_cast<uint32_t>(min(MC_BYTES, bytes(in.side) - in.off));
+    mbar_arrive_expect_tx(&full[s], len);
+    bulk_load(ring + s * MC_BYTES, src(in.side) + from * bytes(in.side) + in.off, len, &full[s]);
+    const int64_t row = in.at;
+    next(in);
+    if (in.at != row) {
+      from = ahead;
+      if (in.at + blocks < v.M) ahead = __ldg(v.perm + in.at + blocks);
+    }
+  };
+  for (int s = 0; s < MC_SLOTS - 1; ++s) load();
+  while (n_out < n_in) {
+    const int s = n_out % MC_SLOTS;
+    if (!mbar_wait(&full[s], (n_out / MC_SLOTS) & 1)) break;
+    ++n_out;
+    const uint32_t len = static_cast<uint32_t>(min(MC_BYTES, bytes(out.side) - out.off));
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                     dst(out.side) + out.at * bytes(out.side) + out.off),
+                 "r"(smem_u32(ring + s * MC_BYTES)), "r"(len)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    next(out);
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the slot before this one has been read
+    load();
+  }
+  for (; n_out < n_in; ++n_out) mbar_wait(&full[n_out % MC_SLOTS], (n_out / MC_SLOTS) & 1);  // after a wait that gave up
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -340,16 +374,26 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 template <int RP, bool kKN>
-__global__ void __launch_bounds__(MS_THREADS) multi_shrink_kernel(const ShrinkParams p, const PlanView v) {
+__global__ void __launch_bounds__(MS_THREADS, RP <= 64 ? 3 : 2)
+    multi_shrink_kernel(const __grid_constant__ ShrinkParams p, const __grid_constant__ PlanView v) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   constexpr int kStages = ms_stages<RP>();
   constexpr int kStage = ms_stage_bytes<RP, kKN>();
   constexpr int kBPitch = ms_b_pitch<RP, kKN>();
+  static_assert(kStages * kStage >= MC_SLOTS * (MC_BYTES + 8), "the copies' ring");
   pdl_launch_dependents();
   if (p.zero != nullptr)
     for (int64_t q = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * MS_THREADS + threadIdx.x;
          q < p.zero_len / 4; q += static_cast<int64_t>(gridDim.x) * gridDim.y * MS_THREADS)
       reinterpret_cast<float4*>(p.zero)[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int tile_blocks = static_cast<int>(gridDim.x) - p.sort.blocks;
+  if (static_cast<int>(blockIdx.x) >= tile_blocks) {
+    if (blockIdx.z == 0 && threadIdx.x == 0 && !__ldg(&v.head->in_order))
+      sort_rows(p.sort, v, static_cast<int>(blockIdx.y) * p.sort.blocks + static_cast<int>(blockIdx.x) - tile_blocks,
+                p.sort.blocks * static_cast<int>(gridDim.y), smem_raw);
+    pdl_wait();
+    return;
+  }
   const int n_tiles = __ldg(&v.head->tiles);
   const PlanTile tile = plan_load(v.tiles + blockIdx.x);  // allocated for every block; garbage past n_tiles
   if (static_cast<int>(blockIdx.x) >= n_tiles) {

@@ -1625,9 +1625,7 @@ int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st
 }
 
 // Sorted copies of X (and dY) for batches that are not in the groups' order.
-int sort_rows(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_t* Ds, int64_t d_width,
-              const PlanView& v, cudaStream_t st) {
-  LaunchScope ls(QLORA_KERNEL_AUX, st);
+SortParams sort_params(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_t* Ds, int64_t d_width) {
   SortParams p{};
   p.src[0] = static_cast<const uint4*>(X);
   p.dst[0] = reinterpret_cast<uint4*>(Xs);
@@ -1635,16 +1633,14 @@ int sort_rows(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_
   p.src[1] = static_cast<const uint4*>(D);
   p.dst[1] = reinterpret_cast<uint4*>(Ds);
   p.vecs[1] = static_cast<int>(d_width / 8);
-  const int64_t most = MC_PER_SM * sm_count();
-  const dim3 grid(static_cast<unsigned>(v.M < most ? v.M : most));
-  return launch_dependent(multi_sort_rows_kernel, grid, MC_THREADS, 0, st, p, v);
+  return p;
 }
 
 template <int RP, bool kKN>
 int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, bool first, cudaStream_t st) {
   constexpr int smem = ms_stages<RP>() * ms_stage_bytes<RP, kKN>();
   if (set_smem_once<multi_shrink_kernel<RP, kKN>>(smem) != QLORA_OK) return QLORA_ERR_CUDA;
-  const dim3 grid(static_cast<unsigned>(max_tiles(v.M, v.n)), static_cast<unsigned>(splits),
+  const dim3 grid(static_cast<unsigned>(max_tiles(v.M, v.n) + p.sort.blocks), static_cast<unsigned>(splits),
                   static_cast<unsigned>(div_up(p.r, MS_MAX_RP)));
   LaunchScope ls(QLORA_KERNEL_TGEMM, st);
   if (!first) return launch_dependent(multi_shrink_kernel<RP, kKN>, grid, MS_THREADS, smem, st, p, v);
@@ -1658,7 +1654,7 @@ int launch_shrink_as(const ShrinkParams& p, int splits, const PlanView& v, bool 
 // while the one before them ends, and wait for it before they read its results.
 template <bool kKN>
 int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, const PlanView& v, bool first,
-                  cudaStream_t st, float* zero = nullptr, int64_t zero_len = 0) {
+                  cudaStream_t st, float* zero = nullptr, int64_t zero_len = 0, const SortParams* sort = nullptr) {
   const int splits = shrink_splits(v.M, v.n, K);
   ShrinkParams p{};
   p.A = static_cast<const uint16_t*>(A);
@@ -1671,6 +1667,11 @@ int launch_shrink(const void* A, const void* B, int64_t K, int r, float* P, cons
   p.P = P;
   p.zero = zero;
   p.zero_len = zero_len;
+  if (sort) {
+    p.sort = *sort;
+    const int64_t blocks = MC_PER_SM * sm_count();
+    p.sort.blocks = static_cast<int>(div_up(v.M < blocks ? v.M : blocks, splits));
+  }
   if (r <= 16) return launch_shrink_as<16, kKN>(p, splits, v, first, st);
   if (r <= 32) return launch_shrink_as<32, kKN>(p, splits, v, first, st);
   if (r <= 64) return launch_shrink_as<64, kKN>(p, splits, v, first, st);
@@ -1969,8 +1970,8 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
   rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
-  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, nullptr, nullptr, 0, v, st);
-  if (rc == QLORA_OK) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
+  const SortParams sort = sort_params(X, w.Xs, h, nullptr, nullptr, 0);
+  if (rc == QLORA_OK) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st, nullptr, 0, &sort);
   if (rc != QLORA_OK) return rc;
   PackJob j{};
   j.P = w.PT;
@@ -1999,8 +2000,8 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
-  if (rc == QLORA_OK) rc = sort_rows(X, w.Xs, h, dY, w.Ds, o, v, st);
-  if (rc == QLORA_OK) rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, false, st);
+  const SortParams sort = sort_params(X, w.Xs, h, dY, w.Ds, o);
+  if (rc == QLORA_OK) rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, false, st, nullptr, 0, &sort);
   if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
   if (rc != QLORA_OK) return rc;
   PackJob ju{}, jt{};
