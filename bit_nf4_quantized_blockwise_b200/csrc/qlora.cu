@@ -248,6 +248,22 @@ int set_smem_once(int bytes) {
   return QLORA_OK;
 }
 
+// A kernel as the programmatic dependent of the one before it on the stream.
+template <typename K, typename... Args>
+int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 int check_wq(const qlora_nf4_t* Wq) {
   if (!Wq) return QLORA_ERR_NULL;
   if (!Wq->codes) return QLORA_ERR_NULL;
@@ -397,7 +413,8 @@ LoraWs lora_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int r, bool b
 }
 
 // Dequantizes the whole weight to bf16 W'^T [o][h] (the same kernel as qlora_dequant).
-int dequant_into(const qlora_nf4_t* Wq, uint16_t* out, int family, cudaStream_t st) {
+// dependent: as the programmatic dependent of the kernel before it, of which it needs nothing.
+int dequant_into(const qlora_nf4_t* Wq, uint16_t* out, int family, cudaStream_t st, bool dependent = false) {
   DequantParams p{};
   p.codes = reinterpret_cast<const uint32_t*>(Wq->codes);
   p.absmax_fp8 = Wq->absmax_fp8;
@@ -412,6 +429,8 @@ int dequant_into(const qlora_nf4_t* Wq, uint16_t* out, int family, cudaStream_t 
   const int64_t grid = grid_for(p.nwords, kDequantThreads * kDequantWords, sm_count());
   {
     LaunchScope ls(family, st);
+    if (dependent)
+      return launch_dependent(nf4_dequant_kernel, dim3(static_cast<unsigned>(grid)), kDequantThreads, kDequantSmem, st, p);
     nf4_dequant_kernel<<<static_cast<unsigned>(grid), kDequantThreads, kDequantSmem, st>>>(p);
   }
   return launch_status();
@@ -1608,22 +1627,6 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
   return w;
 }
 
-// A kernel as the programmatic dependent of the one before it on the stream.
-template <typename K, typename... Args>
-int launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
-}
-
 // Sorted copies of X (and dY) for batches that are not in the groups' order.
 SortParams sort_params(const void* X, uint16_t* Xs, int64_t width, const void* D, uint16_t* Ds, int64_t d_width) {
   SortParams p{};
@@ -1969,9 +1972,11 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
-  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
+  // the rank-r product first: the dequantization, which needs nothing of it and whole SMs, then starts on
+  // each SM as that ends there (333 tokens, 13824 x 5120: 125 -> 121 us a call)
   const SortParams sort = sort_params(X, w.Xs, h, nullptr, nullptr, 0);
-  if (rc == QLORA_OK) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st, nullptr, 0, &sort);
+  rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, true, st, nullptr, 0, &sort);
+  if (rc == QLORA_OK) rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st, true);
   if (rc != QLORA_OK) return rc;
   PackJob j{};
   j.P = w.PT;
@@ -1999,10 +2004,10 @@ int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY,
   PlanView v;
   plan_layout(const_cast<void*>(plan), M, ad->n, &v);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st);
   const SortParams sort = sort_params(X, w.Xs, h, dY, w.Ds, o);
-  if (rc == QLORA_OK) rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, false, st, nullptr, 0, &sort);
+  rc = launch_shrink<false>(dY, ad->L2, o, r, w.PU, v, true, st, nullptr, 0, &sort);
   if (rc == QLORA_OK && !T_saved) rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, false, st);
+  if (rc == QLORA_OK) rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st, true);
   if (rc != QLORA_OK) return rc;
   PackJob ju{}, jt{};
   ju.P = w.PU;

@@ -513,6 +513,7 @@ __global__ void __launch_bounds__(kDequantThreads, 1) nf4_dequant_kernel(const _
   const uint32_t toff = pair_tab_offset(dsmem);
   if (toff + kPairTabBytes > dynamic_smem_bytes()) {
     if (threadIdx.x == 0) atomicOr(&g_status, kStatusSmemLayout);
+    pdl_wait();
     return;
   }
   uint8_t* tab = dsmem + toff;
@@ -543,6 +544,7 @@ __global__ void __launch_bounds__(kDequantThreads, 1) nf4_dequant_kernel(const _
       if (i < p.nwords) __stcs(p.out + i, word_dequant(w[u], key, dup_f32x2(c)));
     }
   }
+  pdl_wait();  // as a programmatic dependent: its completion implies that of the kernel before it
 }
 
 }  // namespace qlora
