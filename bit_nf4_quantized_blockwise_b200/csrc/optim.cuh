@@ -330,12 +330,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Square root and reciprocal to 1 ulp; subnormal arguments count as 0.
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+// A product that no later addition may be fused with: a packed mul and add are contracted even where
+// both are .rn, a sum with +0 is not.
+__device__ __forceinline__ uint64_t mul2_rn(uint64_t a, uint64_t b) { return fma2(a, b, 0ull); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+
+// Reciprocal to 1 ulp; subnormal arguments count as 0.
 __device__ __forceinline__ float rcp_approx(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -407,12 +411,13 @@ struct MultiLoads {
 // block of the tensor before it computes the present one.
 //   32 bits: adamw_kernel's order and rounding (fp32 IEEE throughout), so the
 //   result is that of qlora_adamw_step bit for bit; bound by DRAM.
-//   8 bits: with IEEE square roots and divisions the kernel is bound by
-//   instruction issue, not by DRAM (a step over 160 M parameters: 990 us; with
-//   the approximate root, reciprocal and packed fused multiply-adds below 632 us,
-//   3.5 GB at 5.6 TB/s); they cost 4 ulp of the update, far below p's own
-//   rounding.  A ring of three or four blocks a warp in shared memory, filled by
-//   cp.async, was slower (716 to 802 us for 684 then).
+//   8 bits: with IEEE divisions too the kernel is bound by instruction issue,
+//   not by DRAM (a step over 160 M parameters: 990 us; with an approximate
+//   reciprocal, which costs 4 ulp of the update, far below p's own rounding, and
+//   packed operations 643 us).  An approximate root would save 15 us more,
+//   but moves values over the codes' rounding boundaries.  A ring of three or
+//   four blocks a warp in shared memory, filled by cp.async, was slower (716 to
+//   802 us for 684 then).
 template <bool k8, typename G>
 __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
     multi_adamw_kernel(const __grid_constant__ MultiAdamWParams a, const __grid_constant__ GradPtrs gp) {
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
   pdl_wait();  // coefficients, and the step before this one
   const float clip = __ldcg(&a.head->clip);
   const uint64_t clip2 = dup_f32x2(clip), one_m_b1_2 = dup_f32x2(one_m_b1), minus1_2 = dup_f32x2(-1.0f);
-  const uint64_t b2s_2 = dup_f32x2(a.beta2 * 0x1p24f), one_m_b2s_2 = dup_f32x2(one_m_b2 * 0x1p24f);
+  const uint64_t b2_2 = dup_f32x2(a.beta2), one_m_b2_2 = dup_f32x2(one_m_b2);
   const uint64_t eps_2 = dup_f32x2(a.eps), decay_2 = dup_f32x2(decay);
   int t = multi_find(a, b1 - 1);
   for (int64_t top = b1; top > b0; --t) {
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
     }
     const float step_size = __ldcg(&a.coef[t].step_size);
     const float root = __ldcg(k8 ? &a.coef[t].bc2_inv : &a.coef[t].bc2_sqrt);
-    const uint64_t root_2 = dup_f32x2(root * 0x1p-12f), minus_step_2 = dup_f32x2(-step_size);
+    const uint64_t root_2 = dup_f32x2(root), minus_step_2 = dup_f32x2(-step_size);
     const bool vec = vec_ok(ts.p, 16) && vec_ok(ts.copy, 8), gvec = vec_ok(g, 4 * sizeof(G));
     auto left_of = [&](int64_t b) -> int {
       const int64_t n = ts.n - (b - ts.block0) * MA_BLOCK;
@@ -473,18 +478,18 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
       float(&p)[8] = cur.p;
       float m[8], r[8], v[8];
       if constexpr (k8) {
-        // Two elements an instruction (f32x2).  v is kept times 2^24 (its factors are), so that the
-        // root, which takes subnormal arguments as 0, loses none; r then is times 2^12.
+        // Two elements an instruction (f32x2).  m, v and the root are rounded operation by operation, as
+        // IEEE arithmetic does: a value that falls on the other side of a rounding boundary of its code
+        // changes by a whole code, and the next step's p with it.
         state_decode(cur.mw, cur.ms, m);
         state_decode(cur.vw, cur.vs, r);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const uint64_t g2 = mul2(pack2(cur.g[j], cur.g[j + 1]), clip2), m0 = pack2(m[j], m[j + 1]);
-          const uint64_t m2 = fma2(one_m_b1_2, fma2(m0, minus1_2, g2), m0);
+          const uint64_t g2 = mul2_rn(pack2(cur.g[j], cur.g[j + 1]), clip2), m0 = pack2(m[j], m[j + 1]);
+          const uint64_t m2 = add2(m0, mul2_rn(one_m_b1_2, fma2(m0, minus1_2, g2)));
           const uint64_t r0 = pack2(r[j], r[j + 1]);
-          const uint64_t v2 = fma2(mul2(b2s_2, r0), r0, mul2(mul2(one_m_b2s_2, g2), g2));
-          unpack2(v2, r[j], r[j + 1]);
-          r[j] = sqrt_approx(r[j]), r[j + 1] = sqrt_approx(r[j + 1]);
+          unpack2(add2(mul2_rn(mul2(r0, r0), b2_2), mul2_rn(mul2(g2, g2), one_m_b2_2)), r[j], r[j + 1]);
+          r[j] = __fsqrt_rn(r[j]), r[j + 1] = __fsqrt_rn(r[j + 1]);
           float d0, d1;
           unpack2(fma2(pack2(r[j], r[j + 1]), root_2, eps_2), d0, d1);
           const uint64_t q2 = mul2(m2, pack2(rcp_approx(d0), rcp_approx(d1)));
@@ -530,8 +535,7 @@ __global__ void __launch_bounds__(MA_THREADS, k8 ? MA_PER_SM8 : MA_PER_SM32)
         }
         float ms, minv, rs, rinv;
         block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mtop)), ms, minv);
-        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rtop * 0x1p-12f)), rs, rinv);
-        rinv *= 0x1p-12f;  // r is times 2^12
+        block_scale(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(rtop)), rs, rinv);
         const uint2 mw = state_encode<false>(m, minv), vw = state_encode<true>(r, rinv);
         uint32_t* mc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + b * MA_BLOCK) + lane;
         uint32_t* vc = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + b * MA_BLOCK) + lane;

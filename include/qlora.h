@@ -384,7 +384,10 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
  *   state a NaN's m and r are NaN too, and an infinity makes m of its whole
  *   block NaN and r NaN or infinite, so that the next step's result is NaN there.
  * With 32-bit state the results are those of qlora_adamw_step bit for bit; with
- * 8-bit state the root and the quotient of the update are good to 4 ulp.     */
+ * 8-bit state m, v, r, scales and codes are rounded as IEEE fp32 arithmetic
+ * rounds the formulas above operation by operation (m + (1 - beta1) (g - m),
+ * beta2 v + (1 - beta2) (g g), v = r r), and the update's quotient is good to
+ * 4 ulp.                                                                     */
 #define QLORA_STATE_BLOCK 256
 typedef struct qlora_adamw_tensor_t {
     float*    param;

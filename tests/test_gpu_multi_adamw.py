@@ -261,6 +261,39 @@ def test_nonfinite_gradient_stays_in_its_element_or_block(bits, value):
     assert bad == (list(range(256, 512)) if bits == 8 and value == float("inf") else [300])
 
 
+def _encode(x, floor):
+    """E4M3 codes and scales of blocks of 256 by fp32 operations on the CPU."""
+    top = x.abs().amax(1)
+    y = x * (torch.full_like(top, 448.0) / top)[:, None]
+    if floor:
+        y = torch.where((y > 0) & (y < 2.0 ** -9), torch.full_like(y, 2.0 ** -9), y)
+    return y.to(torch.float8_e4m3fn), top / torch.full_like(top, 448.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_codes_and_scales_are_those_of_ieee_arithmetic(dtype):
+    """Bit for bit over several steps: a value on the other side of a rounding boundary would be a
+    whole code off, and the next step's parameter with it.  400 thousand elements a step."""
+    shapes = [(1000, 256), (600, 256)]
+    opt = MultiAdamW(_tensors(shapes), CFG, state_bits=8)
+    m = v = torch.zeros(1600, 256)
+    b1, b2 = f32(CFG.beta1), f32(CFG.beta2)
+    c1, c2 = float(np.float32(1) - np.float32(b1)), float(np.float32(1) - np.float32(b2))
+    for t in range(1, 5):
+        grads = _grads(shapes, t, dtype)
+        opt.step(grads)
+        g = torch.cat([x.float().cpu() for x in grads])
+        norm = math.sqrt(float(g.double().square().sum()))
+        g = g * torch.tensor(min(1.0, f32(CFG.max_grad_norm) / (norm + 1e-6)), dtype=torch.float32)
+        m = m + (g - m) * c1
+        r = torch.from_numpy(np.sqrt((v.square() * b2 + (g * g) * c2).numpy()))  # torch's own is not to nearest on the CPU
+        (mc, ms), (rc, rs) = _encode(m, False), _encode(r, True)
+        for got, want in ((opt.m, mc), (opt.v, rc)):
+            assert torch.equal(got.cpu().view(torch.uint8), want.view(-1).view(torch.uint8))
+        assert torch.equal(opt.m_scale.cpu(), ms) and torch.equal(opt.v_scale.cpu(), rs)
+        m, v = mc.float() * ms[:, None], rc.float() * rs[:, None]
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_moments_of_a_nan_gradient_are_nan(bits):
     opt = MultiAdamW(_tensors([(1024,)]), AdamWConfig(lr=1e-3, max_grad_norm=None), state_bits=bits)
