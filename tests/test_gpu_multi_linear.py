@@ -333,6 +333,12 @@ def test_an_adapter_of_nan_keeps_to_its_tokens(M):
     assert not torch.isfinite(Y[~mine]).any() and not torch.isfinite(dX[~mine]).any()
 
 
+@pytest.mark.parametrize("M,h,o", [(70, 5184, 256), (330, 256, 10304)])
+def test_wide_rows_out_of_order(M, h, o):
+    """Rows of a little more than one and two pieces of the sorting copies."""
+    check(Case(M, h, o, 5, 16, kind="mixed", none=0.1, seed=M))
+
+
 def test_large_bank_with_few_of_its_adapters_in_the_batch():
     c = Case(70, 128, 128, 3000, 8, kind="mixed", seed=4)
     c.ids = np.where(c.ids % 3 == 0, 2999, c.ids % 5).astype(np.int32)
