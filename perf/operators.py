@@ -269,12 +269,12 @@ def _encode(x, floor):
     """E4M3 codes and the scale of each block; floor: nothing above 0 becomes 0."""
     b = x.view(-1, STATE_BLOCK)
     top = b.abs().amax(1)
-    dead = top < 2.0 ** -100
-    inv = torch.where(dead, torch.zeros_like(top), torch.full_like(top, E4M3_MAX) / top)
+    live = top >= 2.0 ** -100
+    inv = torch.where(live, torch.full_like(top, E4M3_MAX) / top, torch.zeros_like(top))
     y = b * inv[:, None]
     if floor:
         y = torch.where((y > 0) & (y < 2.0 ** -9), torch.full_like(y, 2.0 ** -9), y)
-    scale = torch.where(dead, torch.zeros_like(top), top / torch.full_like(top, E4M3_MAX))
+    scale = torch.where(live, top / torch.full_like(top, E4M3_MAX), torch.zeros_like(top))
     return y.to(torch.float8_e4m3fn).view(-1), scale
 
 
