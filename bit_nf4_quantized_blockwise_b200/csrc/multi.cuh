@@ -760,7 +760,7 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorM
 struct MultiPairParams {
   PairGemmParams g;         // k_ext_stages is not used: a tile has chunks stages per slot
   int even;                 // no whole rounds: the stages of all tiles in even shares (see below)
-  int chain;                // stages of an accumulator (0: those of the item)
+  int chain;                // stages of an accumulator
   int chunks;               // rp / 64
   int rp, parts;
   const uint16_t* A;        // [M][K], batch order
@@ -966,15 +966,20 @@ constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<in
 // straight from the bank (the forward's L2 is an N-major operand, the
 // backward's L1 a K-major one; ranks past r are zero-filled by the 3-D map).
 // Rows are read in sorted order and written to their own place.
-// The tensor core cuts its running sum to fp32 at every step of a chain.  For a
-// bf16 result that is nothing; for an fp32 one it would be most of its error (K =
-// 11008: 1.1e-5 against 64 bits, an fp32 product 7e-7).  With an fp32 result the
-// accumulator therefore changes every MP_CHAIN stages and the epilogue, eight
-// warps with 128 sums a thread, adds it in registers while the MMAs go on with
-// the other one: 7.6e-7, for 371 us instead of 345 at 4096 x 4096 x 11008 (313 with a
-// bf16 result).  (Running sums in memory instead,
-// 256 KB a pair in L2: 453 us.)
-constexpr int MP_CHAIN = 8;
+// The tensor core cuts its running sum to fp32 at every step (16 products), which
+// adds up over a long accumulator: 11e-6 against 64 bits at K = 11008, where an
+// fp32 sum is 1e-6 off, and a bf16 result then rounds to another value in 0.6 % of
+// the elements of a sum of 8192 positive products.  So the accumulator changes every
+// `chain` stages of 128 products, and the epilogue, eight warps with 128 sums a
+// thread, adds it in registers while the MMAs go on with the other one.  (Running
+// sums in memory instead, 256 KB a pair in L2: 453 us for 345 at 4096 x 4096 x 11008.)
+//   bf16 results: 8 stages (0.07 % there).  One accumulator: 289 us a call of 4096 x
+//   4096 x 11008 with an L2 flushed before it, 16 stages 293, 8 stages 301, 4 stages 328.
+//   fp32 results: as exact as an fp32 sum.  4 stages, 3.4e-7 (fp32 sums of K = 4096:
+//   5.1e-7), 368 us for 344 with 8 stages (7.4e-7); up to K = 2048, where an fp32 sum
+//   is better than that (1.6e-7 at 768) and the product a smaller part of the call, 2
+//   stages, 1.9e-7 (4096 x 4096 x 11008 would take 405 us).
+constexpr int multi_chain(bool out_bf16, int64_t K) { return out_bf16 ? 8 : (K > 2048 ? 4 : 2); }
 constexpr int MG_EPI_WARPS = 8;
 constexpr int MG_PAIR_THREADS = 64 + 32 * MG_EPI_WARPS;
 constexpr int MG_COLS = PG_ACC_COLS / 2;  // columns of an epilogue warp
@@ -1150,7 +1155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
           }
           tc_fence_after();
           const uint32_t d_tmem = tmem + static_cast<uint32_t>(b * PG_ACC_COLS);
-          const int first = i, end = mp.chain > 0 ? min(it.kend, i + mp.chain) : it.kend;
+          const int first = i, end = min(it.kend, i + mp.chain);
           for (; i < end; ++i, ++G) {
             const int s = G % PG_STAGES;
             if (!mbar_wait(&full[s], (G / PG_STAGES) & 1, kTagPgFull)) {
@@ -1211,7 +1216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_even(&tempty[b], rank);
-        i = mp.chain > 0 ? min(it.kend, i + mp.chain) : it.kend;
+        i = min(it.kend, i + mp.chain);
       }
       if (!ok) break;
       const int n0 = it.n0 + c0;

@@ -1760,7 +1760,7 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.full_units = split > 1 ? p.g.units - tail : p.g.units;
   p.g.partial = w.Wpart;
   p.g.counters = w.Wcnt;
-  p.chain = out_bf16 ? 0 : MP_CHAIN;
+  p.chain = multi_chain(out_bf16 != 0, K);
   p.chunks = static_cast<int>(rp / 64);
   p.rp = static_cast<int>(rp);
   p.parts = parts;
