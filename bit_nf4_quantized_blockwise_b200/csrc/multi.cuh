@@ -501,8 +501,8 @@ __global__ void __launch_bounds__(MS_THREADS, RP <= 64 ? 3 : 2)
 
 // Fills the slots of T (or U): the sum of the K parts in order, or a T given by
 // the caller, times the adapter's scale, as `parts` bf16 terms: two keep 16 bits
-// of the value (the W' product adds them to a sum of bf16 products), three 24
-// (the sums over tokens, whose results are fp32).  Also writes T itself in the
+// of the value, which is 256 steps of a bf16 result; three keep 24, for fp32
+// results (those of the W' product, and the sums over tokens).  Also writes T itself in the
 // batch's order, zero for tokens without adapter.  blockIdx.x < max_slots: 64
 // rows (blockIdx.y) of a slot; above: the rows without adapter of a tile.
 struct PackJob {
@@ -758,11 +758,12 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorM
 }
 
 struct MultiPairParams {
-  PairGemmParams g;         // k_ext_stages is not used: a tile has chunks stages per slot
+  PairGemmParams g;         // k_ext_stages is not used: a tile has slot_stages stages per slot
   int even;                 // no whole rounds: the stages of all tiles in even shares (see below)
   int chain;                // stages of an accumulator
-  int chunks;               // rp / 64
-  int rp, parts;
+  int slot_stages;          // two (part, 64 ranks) pairs each
+  int rp, parts;            // of the slots
+  int used;                 // the parts that enter the product, 2 or 3
   const uint16_t* A;        // [M][K], batch order
   const uint16_t* Wd;       // W'^T [o][h]
   const uint16_t* slots;
@@ -826,7 +827,8 @@ __device__ __forceinline__ void multi_elements(const MultiPairParams& p, const u
   const uint16_t* b = p.bank + static_cast<int64_t>(adapter) * p.r * p.g.N;
   float d[8] = {};
   for (int j = 0; j < p.r; ++j) {
-    const float t = bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]);
+    float t = bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]);
+    if (p.used > 2) t += bf16_bits_to_float(row[2 * p.rp + j]);
     if (kBwd) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) d[c] = fmaf(t, bf16_bits_to_float(b[static_cast<int64_t>(n + c) * p.r + j]), d[c]);
@@ -927,7 +929,7 @@ __device__ __forceinline__ int tile_stages(const MultiPairParams& p, const PlanV
   const PairTiles tiles{p.g.units / p.g.n_tiles, p.g.n_tiles};
   int mt, n0;
   tiles.at(u, mt, n0);
-  return p.g.k_main_stages + (v.tile_slot0[mt + 1] - v.tile_slot0[mt]) * p.chunks;
+  return p.g.k_main_stages + (v.tile_slot0[mt + 1] - v.tile_slot0[mt]) * p.slot_stages;
 }
 
 // Calls f(u, first stage, stages) for all tiles, by one warp; returns the sum of the stages.
@@ -961,10 +963,12 @@ constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<in
 
 // pair_gemm_kernel's pipeline (256 x 256 tiles on two-SM clusters, 128-deep
 // stages, two accumulators, K parts for what does not fill a round) with K
-// extended per tile: one stage for every slot of the tile and 64 ranks, A the
-// slot's [hi | mid] and B the same 64 ranks of the group's factor twice,
-// straight from the bank (the forward's L2 is an N-major operand, the
-// backward's L1 a K-major one; ranks past r are zero-filled by the 3-D map).
+// extended per tile, by slot_stages stages for every slot of the tile.  The halves of a
+// stage are 64 ranks of one bf16 part of the slot (A) and the same 64 ranks of the group's
+// factor (B), straight from the bank (the forward's L2 is an N-major operand, the
+// backward's L1 a K-major one; ranks past r are zero-filled by the 3-D map): [hi | mid] of
+// 64 ranks for a bf16 result, hi, mid and lo one after the other for an fp32 one, whose
+// last stage may be half zeros.
 // Rows are read in sorted order and written to their own place.
 // The tensor core cuts its running sum to fp32 at every step (16 products), which
 // adds up over a long accumulator: 11e-6 against 64 bits at K = 11008, where an
@@ -1018,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
     it.part = u >= n_parts ? -1 : u;
     tiles.at(u >= n_parts ? u - n_parts : p.full_units + u / p.split, it.mt, it.n0);
     it.slot0 = v.tile_slot0[it.mt];
-    const int S = KM + (v.tile_slot0[it.mt + 1] - it.slot0) * mp.chunks;
+    const int S = KM + (v.tile_slot0[it.mt + 1] - it.slot0) * mp.slot_stages;
     it.kbeg = 0;
     it.kend = S;
     if (it.part >= 0) {
@@ -1108,22 +1112,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
               tma_load_2d_pair(b_dst + PG_ATOM_BYTES, &tmB, fb, k0 + 64, n0);
             }
           } else {
-            const int e = (i - KM) / mp.chunks;
-            const int x = ((i - KM) - e * mp.chunks) * 64;
+            const int e = (i - KM) / mp.slot_stages;
+            const int j0 = 2 * ((i - KM) - e * mp.slot_stages);
             const int slot = it.slot0 + e;
             const int a = __ldg(&v.slots[slot].adapter);
             const int y = slot * MP_SLOT_ROWS + static_cast<int>(rank) * 128;
-            tma_load_2d_pair(a_dst, &tmAe, fb, x, y);
-            tma_load_2d_pair(a_dst + PG_ATOM_BYTES, &tmAe, fb, mp.rp + x, y);
-            if (kBwd) {
-              // K-major: 64 ranks of 128 rows of L1, once for each half of the stage
-              tma_load_3d_pair(b_dst, &tmBe, fb, x, n0, a);
-              tma_load_3d_pair(b_dst + PG_ATOM_BYTES, &tmBe, fb, x, n0, a);
-            } else {
-              // N-major: per 64 columns of L2 its 64 ranks twice, one below the other
-              for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+              const int j = j0 + h, chunk = j / mp.used;
+              // behind the last pair: past the end of both maps, which read zeros there
+              const bool in = 64 * chunk < mp.rp;
+              const int x = in ? 64 * chunk : mp.rp;
+              tma_load_2d_pair(a_dst + h * PG_ATOM_BYTES, &tmAe, fb, in ? (j - chunk * mp.used) * mp.rp + x : mp.parts * mp.rp, y);
+              if (kBwd) {
+                // K-major: 64 ranks of 128 rows of L1
+                tma_load_3d_pair(b_dst + h * PG_ATOM_BYTES, &tmBe, fb, x, n0, a);
+              } else {
+                // N-major: 64 ranks of each 64 columns of L2, the second half of the stage below the first
                 for (int c = 0; c < 2; ++c)
                   tma_load_3d_pair(b_dst + c * PG_ATOM_BYTES + h * (PG_ATOM_BYTES / 2), &tmBe, fb, n0 + 64 * c, x, a);
+              }
             }
           }
         }

@@ -1593,7 +1593,7 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
     return q;
   };
   const int64_t pairs = (sm_count() + 1) / 2;
-  const int64_t slot_bytes = max_slots(M, n) * MP_SLOT_ROWS * rank_pad(r) * (bwd ? 3 : 2) * 2;
+  const int64_t slot_bytes = max_slots(M, n) * MP_SLOT_ROWS * rank_pad(r) * MD_PARTS * 2;
   MultiWs w{};
   w.PT = static_cast<float*>(take(shrink_splits(M, n, h) * M * r * 4));
   if (!bwd && M <= kMultiDecodeMax) {
@@ -1717,13 +1717,14 @@ int multi_resident_pairs() {
   return n;
 }
 
-// out = A (op W') + the groups' terms.  A [M][K] in batch order, As its sorted copy.
+// out = A (op W') + the groups' terms.  A [M][K] in batch order, As its sorted copy; parts: of the slots.
 template <bool kBwd>
 int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, const qlora_adapters_t* ad,
                       const uint16_t* Wd, int64_t o, int64_t h, int parts, void* out, int out_bf16, const MultiWs& w,
                       const PlanView& v, cudaStream_t st) {
   const int64_t M = v.M, K = kBwd ? o : h, N = kBwd ? h : o;
   const int64_t r = ad->r, rp = rank_pad(ad->r), rows = max_slots(M, v.n) * MP_SLOT_ROWS;
+  const int used = out_bf16 ? 2 : 3, slot_stages = static_cast<int>(div_up(used * (rp / 64), 2));
   CUtensorMap ma, mas, mb, mae, mbe;
   if (!map_bf16(&ma, A, K, M, K * 2, 64, 128) || !map_bf16(&mas, As, K, M, K * 2, 64, 128) ||
       !map_bf16(&mb, Wd, h, o, h * 2, 64, 128) || !map_bf16(&mae, slots, parts * rp, rows, parts * rp * 2, 64, 128))
@@ -1745,9 +1746,9 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.out_bf16 = out_bf16;
   p.g.ld_out = N;
   // Fewer tiles than pairs: even shares, unless they save fewer stages of the longest tile than the
-  // reduction that they need costs (about 8 us, a stage 0.84; a tile has at most one stage for each
-  // group and 64 ranks).
-  const int64_t longest = p.g.k_main_stages + (rp / 64) * (v.n < M ? v.n : (M < PG_BM ? M : PG_BM));
+  // reduction that they need costs (about 8 us, a stage 0.84; a tile has at most slot_stages
+  // for each group).
+  const int64_t longest = p.g.k_main_stages + slot_stages * (v.n < M ? v.n : (M < PG_BM ? M : PG_BM));
   p.even = p.g.units < pairs && longest * (pairs - p.g.units) / pairs > 10 ? 1 : 0;
   // With whole rounds, the tiles of the last one, which would leave pairs without work, are split
   // along K into up to four parts (each at least two stages) that run first.
@@ -1761,9 +1762,10 @@ int launch_multi_pair(const void* A, const uint16_t* As, const uint16_t* slots, 
   p.g.partial = w.Wpart;
   p.g.counters = w.Wcnt;
   p.chain = multi_chain(out_bf16 != 0, K);
-  p.chunks = static_cast<int>(rp / 64);
+  p.slot_stages = slot_stages;
   p.rp = static_cast<int>(rp);
   p.parts = parts;
+  p.used = used;
   p.A = static_cast<const uint16_t*>(A);
   p.Wd = Wd;
   p.slots = slots;
@@ -1983,9 +1985,10 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   j.T = T_save;
   j.slots = w.ST;
   j.splits = shrink_splits(M, ad->n, h);
-  rc = launch_pack(j, nullptr, ad->s, r, 2, w, v, st);
+  const int parts = y_dtype == QLORA_DTYPE_BF16 ? 2 : MD_PARTS;
+  rc = launch_pack(j, nullptr, ad->s, r, parts, w, v, st);
   if (rc != QLORA_OK) return rc;
-  return launch_multi_pair<false>(X, w.Xs, w.ST, ad, w.Wd, o, h, 2, Y, y_dtype == QLORA_DTYPE_BF16, w, v, st);
+  return launch_multi_pair<false>(X, w.Xs, w.ST, ad, w.Wd, o, h, parts, Y, y_dtype == QLORA_DTYPE_BF16, w, v, st);
 }
 
 int qlora_multi_linear_bwd(const qlora_nf4_t* Wq, const void* X, const void* dY, int64_t M,

@@ -284,8 +284,8 @@ int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, siz
  * and n, complete on `stream`; ws: device workspace of
  * qlora_multi_linear_*_workspace_size() bytes (0: sizes the layer does not take).
  * W' is bf16; products are bf16 x bf16 accumulated in fp32.  T and U stay in
- * fp32 and enter the W' product as two bf16 parts (16 bits), the gradients as
- * three (24 bits).  Sums are added in a fixed order and results repeat bit for
+ * fp32 and enter the W' product as bf16 parts: two (16 bits) for a bf16 result,
+ * three (24 bits) for an fp32 one and for the gradients.  Sums are added in a fixed order and results repeat bit for
  * bit, except Y of up to 32 tokens (decode), whose base product is accumulated
  * with fp32 atomics as in qlora_linear_fwd.  A token's outputs depend on its own
  * row and adapter alone, and an adapter's gradients on its own tokens alone,

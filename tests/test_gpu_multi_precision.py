@@ -4,6 +4,7 @@ term, against 64 bits.
 u = 2^-24.  The tensor core cuts its running sum by up to a step of fp32, 2 u of it, at every 16
 products.  Above 32 tokens an accumulator ends after 1024 products (fp32 results: 512, and 256 where
 there are 2048 or fewer) and is added in fp32."""
+import numpy as np
 import pytest
 import torch
 
@@ -71,3 +72,31 @@ def test_fp32_results_are_as_exact_as_fp32_sums(k, steps, bwd):
     got, want = _base(w, x, bwd, torch.float32)
     off = float(((got.double() - want).abs() / want).max()) / U
     assert off <= steps + 1 + k // (16 * steps), off
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("r", [8, 64, 72, 200, 256])
+def test_fp32_results_keep_24_bits_of_the_rank_r_product(r, bwd):
+    """W' = 0; T (or U) = 1 + 2^-9 + 2^-18 in every rank, which two bf16 parts of 8 bits cannot hold,
+    times a factor of 1 in the last 8 ranks and 0 in the others: the result 8 (1 + 2^-9 + 2^-18) and
+    every partial sum of it are fp32 values, and no product lies below the last bit of such a sum, so it
+    has to come out exactly."""
+    M, o, h = 40, 192, 128
+    w = _weight(o, h, torch.full((o * h // 2,), 0x77, device="cuda", dtype=torch.uint8))  # the code of 0
+    assert float(q.qlora_dequant(w).abs().max()) == 0.0
+    L1, L2 = torch.ones(2, h, r), torch.ones(2, r, o)
+    wide, last = (L2.transpose(1, 2), L1) if bwd else (L1, L2.transpose(1, 2))  # [n][o or h][r]
+    wide[:, :3] = torch.tensor([1.0, 2.0 ** -9, 2.0 ** -18])[None, :, None]
+    last[:, :, :r - 8] = 0
+    bank = q.AdapterBank(L1.bfloat16().cuda(), L2.bfloat16().cuda(), torch.ones(2, device="cuda"))
+    plan = q.qlora_adapter_plan(torch.arange(M, device="cuda", dtype=torch.int32) % 2, 2)
+    x = torch.zeros(M, o if bwd else h, device="cuda", dtype=torch.bfloat16)
+    x[:, :3] = 1
+    if bwd:
+        X = torch.zeros(M, h, device="cuda", dtype=torch.bfloat16)
+        y = q.qlora_multi_linear_bwd(w, X, x, bank, plan)[0]
+    else:
+        y = q.qlora_multi_linear_fwd(w, x, bank, plan)[0]
+    want = 8 * (1 + 2.0 ** -9 + 2.0 ** -18)
+    assert float(np.float32(want)) == want
+    assert bool((y == want).all()), (y.min().item(), y.max().item(), want)
