@@ -20,9 +20,10 @@
 //
 // Zero rows keep the groups apart only while the factors are finite: 0 times an
 // infinity or a NaN of another group's adapter (or of another token, in the
-// sums over tokens) is NaN.  Every element of a tile that several groups share
-// that comes out non-finite is therefore computed once more from its own row
-// and adapter alone, in fp32; a finite batch never gets there.
+// sums over tokens) is NaN.  And a value in parts, hi inf + mid inf, is NaN where the
+// value itself times inf is not.  Every element that comes out non-finite is
+// therefore computed once more from its own row and adapter alone, in fp32 and
+// with whole values; a finite batch never gets there.
 #pragma once
 
 #include "qlora.h"
@@ -803,10 +804,9 @@ __device__ __forceinline__ const uint16_t* slot_row(const MultiPairParams& p, co
   return nullptr;
 }
 
-// Eight elements n .. n + 7 from their own row and adapter alone, in fp32.
+// Eight elements n .. n + 7 from their own row and adapter alone, in fp32: the base sum,
 template <bool kBwd>
-__device__ __forceinline__ void multi_elements(const MultiPairParams& p, const uint16_t* a, const uint16_t* row,
-                                               int adapter, int n, float (&x)[8]) {
+__device__ __forceinline__ void base_elements(const MultiPairParams& p, const uint16_t* a, int n, float (&x)[8]) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) x[c] = 0.0f;
   for (int k = 0; k < p.K; k += 8) {  // K is a multiple of 64
@@ -823,9 +823,15 @@ __device__ __forceinline__ void multi_elements(const MultiPairParams& p, const u
         x[c] = dot8(av, *reinterpret_cast<const uint4*>(p.Wd + static_cast<int64_t>(n + c) * p.K + k), x[c]);
     }
   }
-  if (!row) return;
+}
+
+// and the adapter's term.
+template <bool kBwd>
+__device__ __forceinline__ void adapter_elements(const MultiPairParams& p, const uint16_t* row, int adapter, int n,
+                                                 float (&d)[8]) {
   const uint16_t* b = p.bank + static_cast<int64_t>(adapter) * p.r * p.g.N;
-  float d[8] = {};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) d[c] = 0.0f;
   for (int j = 0; j < p.r; ++j) {
     float t = bf16_bits_to_float(row[j]) + bf16_bits_to_float(row[p.rp + j]);
     if (p.used > 2) t += bf16_bits_to_float(row[2 * p.rp + j]);
@@ -836,16 +842,6 @@ __device__ __forceinline__ void multi_elements(const MultiPairParams& p, const u
       axpy8(t, *reinterpret_cast<const uint4*>(b + static_cast<int64_t>(j) * p.g.N + n), d);
     }
   }
-#pragma unroll
-  for (int c = 0; c < 8; ++c) x[c] += d[c];
-}
-
-// Whether rows of several owners (groups, or none) meet in a 256-row tile.
-__device__ __forceinline__ bool tile_shared(const MultiPairParams& p, const PlanView& v, int mt) {
-  const int s0 = v.tile_slot0[mt], ns = v.tile_slot0[mt + 1] - s0;
-  if (ns != 1) return ns > 1;
-  const PlanSlot ps = plan_load(v.slots + s0);
-  return ps.start > mt * PG_BM || ps.end < min((mt + 1) * PG_BM, p.g.M);
 }
 
 // Whether all of x is finite: x 0 is 0 then, so one fused multiply-add each tells.
@@ -858,14 +854,18 @@ __device__ __forceinline__ bool all_finite(const float* x) {
 }
 
 // Replaces what is not finite among the `len` elements (a multiple of 8) from n on that this thread
-// has stored of sorted row m by its own sum; nothing to do where the row itself is not finite, or its
-// product with its adapter's first factor is NaN (then all its elements are).  So a batch of NaN costs
-// a look at its rows, and one adapter of infinities, or sums that overflow, 12 to 20 ms at 4096 x 4096 x
-// 11008 (eight elements at a time, so that each load of the row and of W' serves eight).  Never
+// has stored of sorted row m by its own sum.  Nothing to do in a tile without adapters, nor where the
+// row, or its product with its adapter's first factor, holds a NaN: all its elements are NaN then,
+// whatever W' and the factors are.  Where the adapter's term is NaN, so is the element, without the long
+// sum.  So a batch of NaN costs a look at its rows (4096 x 4096 x 11008: nothing to be seen) and one with
+// an infinity in every row 5 ms; neighbours of one adapter of infinities take the long sum, eight
+// elements at a time, so that each load of the row and of W' serves eight: 8 ms, the backward 12.  Never
 // inlined: the path is rare and long.
 template <bool kBwd>
 __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanView& v, int m, int n, int len) {
   const uint16_t* a = p.A + static_cast<int64_t>(v.perm[m]) * p.K;
+  const int tile = m / MP_SLOT_ROWS;
+  if (v.tile_slot0[tile] == v.tile_slot0[tile + 1]) return;
   int adapter = -1;
   const uint16_t* row = slot_row(p, v, m, adapter);
   if (row)
@@ -875,8 +875,8 @@ __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanVi
     const uint4 x = *reinterpret_cast<const uint4*>(a + k);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // an exponent of ones in either half
-      if ((w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u) return;
+    for (int i = 0; i < 4; ++i)
+      if (isnan(__uint_as_float(w[i] << 16)) || isnan(__uint_as_float(w[i] & 0xFFFF0000u))) return;
   }
   const int64_t at = static_cast<int64_t>(v.perm[m]) * p.g.ld_out + n;
   uint16_t* o16 = static_cast<uint16_t*>(p.g.out) + at;
@@ -886,15 +886,23 @@ __device__ __noinline__ void multi_repair(const MultiPairParams& p, const PlanVi
     for (int c = 0; c < 8; ++c)
       if (!isfinite(p.g.out_bf16 ? bf16_bits_to_float(o16[t + c]) : o32[t + c])) bad |= 1u << c;
     if (bad == 0) continue;
-    float x[8];
-    multi_elements<kBwd>(p, a, row, adapter, n + t, x);
+    float x[8], d[8] = {};
+    if (row) adapter_elements<kBwd>(p, row, adapter, n + t, d);
+    bool any = false;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) any = any || ((bad >> c & 1) && !isnan(d[c]));
+    if (any) {
+      base_elements<kBwd>(p, a, n + t, x);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) d[c] += x[c];
+    }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       if (!(bad >> c & 1)) continue;
       if (p.g.out_bf16)
-        o16[t + c] = __bfloat16_as_ushort(__float2bfloat16_rn(x[c]));
+        o16[t + c] = __bfloat16_as_ushort(__float2bfloat16_rn(d[c]));
       else
-        o32[t + c] = x[c];
+        o32[t + c] = d[c];
     }
   }
 }
@@ -1273,8 +1281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MG_PAIR_THREADS, 1)
         for (int j = 0; j < MG_COLS; j += 4)
           if (n0 + j < p.N) __stcs(reinterpret_cast<float4*>(out + j), make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]));
       }
-      if (tile_shared(mp, v, it.mt) && !all_finite<MG_COLS>(x))
-        multi_repair<kBwd>(mp, v, m, n0, min(MG_COLS, p.N - n0));
+      if (!all_finite<MG_COLS>(x)) multi_repair<kBwd>(mp, v, m, n0, min(MG_COLS, p.N - n0));
     }
   }
 
@@ -1321,7 +1328,6 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
   pdl_wait();
   if (c0 == c1) return;  // one pair computed the whole tile and has stored it
   const int64_t place0 = 2 * c0 + (at > stage_share(all, c0, pairs).lo ? 1 : 0);
-  const bool shared = tile_shared(mp, v, mt);
   const float4* first = reinterpret_cast<const float4*>(p.partial + place0 * PG_BM * PG_BN);
   const float4* rest = reinterpret_cast<const float4*>(p.partial);
   // 8 columns of a row a thread; the places are [4 columns][row]
@@ -1349,7 +1355,7 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
       out[0] = x[0], out[1] = x[1];
     }
     const float all[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    if (shared && !all_finite<8>(all)) multi_repair<kBwd>(mp, v, m, n0 + c, 8);
+    if (!all_finite<8>(all)) multi_repair<kBwd>(mp, v, m, n0 + c, 8);
   }
 }
 

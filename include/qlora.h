@@ -288,8 +288,8 @@ int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, siz
  * three (24 bits) for an fp32 one and for the gradients.  Sums are added in a fixed order and results repeat bit for
  * bit, except Y of up to 32 tokens (decode), whose base product is accumulated
  * with fp32 atomics as in qlora_linear_fwd.  A token's outputs depend on its own
- * row and adapter alone, and an adapter's gradients on its own tokens alone,
- * infinities and NaN included.                                              */
+ * row and adapter alone, and an adapter's gradients on its own tokens alone: which
+ * elements are +inf, -inf or NaN exactly, finite ones up to the order of their sums. */
 size_t qlora_multi_linear_fwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
 size_t qlora_multi_linear_bwd_workspace_size(int64_t o, int64_t h, int64_t M, int n, int r);
 int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, const qlora_adapters_t* adapters,
