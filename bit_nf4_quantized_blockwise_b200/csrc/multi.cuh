@@ -1410,7 +1410,8 @@ struct MultiGradParams {
 
 // Replaces what is not finite among the `ranks` elements (a multiple of 8) of row m of a factor's
 // gradient, from rank j0 on, that this thread has stored at out (`ld` apart) by the sum over the group's
-// own tokens, in fp32, eight ranks at a time.  Never inlined: the path is rare and long.
+// own tokens with the whole values of U or T, in fp32, eight ranks at a time, up to where all of them
+// are NaN.  Never inlined: the path is rare and long.
 __device__ __noinline__ void grad_repair(const MultiGradSide& side, const PlanView& v, int grp, int rp, int m, int j0,
                                          int ranks, float* out, int64_t ld) {
   const PlanGroup pg = plan_load(v.groups + grp);
@@ -1423,6 +1424,12 @@ __device__ __noinline__ void grad_repair(const MultiGradSide& side, const PlanVi
     float x[8] = {};
 #pragma unroll 4
     for (int row = pg.start; row < pg.end; ++row) {
+      if ((row - pg.start) % 64 == 63) {
+        bool ended = true;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) ended = ended && (isnan(x[c]) || !(bad >> c & 1));
+        if (ended) break;
+      }
       const int64_t slot_row = (slot0 + row / MP_SLOT_ROWS) * MP_SLOT_ROWS + row % MP_SLOT_ROWS;
       const uint16_t* b = side.slots + slot_row * (MD_PARTS * rp) + j0 + t;
       const uint4 hi = *reinterpret_cast<const uint4*>(b), mid = *reinterpret_cast<const uint4*>(b + rp),
@@ -1640,9 +1647,7 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
         for (int j = 0; j < MD_BN; j += 4)
           if (j < ranks) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
       }
-      // rows of others in the group's first or last block
-      if (it.grp >= 0 && (it.pg.start % MD_BK != 0 || (it.pg.end % MD_BK != 0 && it.pg.end < v.M)) &&
-          !all_finite<MD_BN>(x)) {
+      if (it.grp >= 0 && !all_finite<MD_BN>(x)) {
         if (it.second)
           grad_repair(side, v, it.grp, p.rp, m, it.j0, ranks, out + static_cast<int64_t>(it.j0) * side.rows + m, side.rows);
         else

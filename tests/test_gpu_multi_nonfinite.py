@@ -47,7 +47,7 @@ def _same(got, want, bound, what):
     assert np.all(np.abs(got[fine] - want[fine]) <= bound[fine] + 1e-30), what
 
 
-def _check(c, spoil, dtype=torch.float32, grads=False):
+def _check(c, spoil, dtype=torch.float32, grads=True):
     _, bY, _, _ = c.forward()
     _, bX, _, b1, _, b2 = c.backward()
     spoil(c)
@@ -119,4 +119,4 @@ def test_bf16_results(what):
 @pytest.mark.parametrize("what", ["rows", "own L2"])
 def test_more_tiles_than_pairs(what):
     """Tiles of whole rounds and of the split last one."""
-    _check(Case(2100, 512, 2368, 3, 8, kind="mixed", none=0.1, seed=6), SPOILS[what])
+    _check(Case(2100, 512, 2368, 3, 8, kind="mixed", none=0.1, seed=6), SPOILS[what], grads=False)
