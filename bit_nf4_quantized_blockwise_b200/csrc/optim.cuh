@@ -131,9 +131,9 @@ struct MultiTensor {
 };
 
 struct MultiCoef {
-  float step_size;  // lr / (1 - beta1^t), t the tensor's own step count
+  float step_size;  // unit lr / (1 - beta1^t), t the tensor's own step count
   float bc2_sqrt;   // sqrt(1 - beta2^t)
-  float bc2_inv;    // 1 / sqrt(1 - beta2^t)
+  float bc2_inv;    // unit / sqrt(1 - beta2^t)
 };
 
 // Device side of a plan, in this order in one allocation.
@@ -160,6 +160,7 @@ struct MultiAdamWParams {
   float lr, beta1, beta2, eps, weight_decay, max_grad_norm;
   int clip;               // clip by the global norm
   int share;              // CTAs that take the blocks of one contiguous range in turn
+  float unit;             // 8 bits: a power of two that eps, the root's factor and the step carry (see the update)
 };
 
 struct GradPtrs {
@@ -245,10 +246,10 @@ __global__ void __launch_bounds__(MA_THREADS) multi_adamw_prepare_kernel(const _
       if (!multi_grad(a, gp, t)) continue;
       const int k = ++a.steps[t];
       MultiCoef c;
-      c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k)));
+      c.step_size = static_cast<float>(static_cast<double>(a.lr) / (1.0 - pow(static_cast<double>(a.beta1), k))) * a.unit;
       const double root = sqrt(1.0 - pow(static_cast<double>(a.beta2), k));
       c.bc2_sqrt = static_cast<float>(root);
-      c.bc2_inv = static_cast<float>(1.0 / root);
+      c.bc2_inv = static_cast<float>(1.0 / root) * a.unit;
       a.coef[t] = c;
     }
   double s = 0.0;
@@ -414,7 +415,9 @@ struct MultiLoads {
 //   8 bits: with IEEE divisions too the kernel is bound by instruction issue,
 //   not by DRAM (a step over 160 M parameters: 990 us; with an approximate
 //   reciprocal, which costs 4 ulp of the update, far below p's own rounding, and
-//   packed operations 643 us).  An approximate root would save 15 us more,
+//   packed operations 643 us).  The reciprocal reads a subnormal number as 0 and gives 0 for one:
+//   where eps is near either end of fp32, eps, the root's factor and the step are multiplied by a power
+//   of two, exactly.  An approximate root would save 15 us more,
 //   but moves values over the codes' rounding boundaries.  A ring of three or
 //   four blocks a warp in shared memory, filled by cp.async, was slower (716 to
 //   802 us for 684 then).

@@ -1379,6 +1379,8 @@ int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t sta
   a.weight_decay = hp->weight_decay;
   a.max_grad_norm = hp->max_grad_norm;
   a.clip = hp->max_grad_norm > 0.0f ? 1 : 0;
+  a.unit = state->bits == 32 ? 1.0f : (hp->eps < 0x1p-100f ? 0x1p24f : (hp->eps > 0x1p100f ? 0x1p-24f : 1.0f));
+  a.eps *= a.unit;
   GradPtrs gp{};
   if (!a.from_memory) {
     std::memcpy(gp.g, grads, sizeof(void*) * static_cast<size_t>(count));
