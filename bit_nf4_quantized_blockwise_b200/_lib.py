@@ -43,7 +43,7 @@ class qlora_adamw_tensor_t(ctypes.Structure):
 class qlora_adamw_state_t(ctypes.Structure):
     """Mirror of the C struct qlora_adamw_state_t."""
     _fields_ = [("m", _c_void_p), ("v", _c_void_p), ("m_scale", _c_void_p), ("v_scale", _c_void_p),
-                ("steps", _c_void_p), ("bits", ctypes.c_int32)]
+                ("steps", _c_void_p), ("bits", ctypes.c_int32), ("rounding", ctypes.c_int32)]
 
 
 class qlora_adapters_t(ctypes.Structure):

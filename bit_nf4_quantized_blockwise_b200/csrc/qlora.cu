@@ -1253,7 +1253,7 @@ MultiPlan multi_plan_layout(void* base, int count, int64_t blocks) {
 
 constexpr int kMaxTensors = 1 << 20;
 
-template <bool k8, typename G>
+template <bool k8, bool kStochastic, typename G>
 int launch_multi_adamw(MultiAdamWParams a, const GradPtrs& gp, int64_t blocks, cudaStream_t st) {
   const int64_t ctas = (blocks + MA_WARPS - 1) / MA_WARPS;
   const int64_t most = static_cast<int64_t>(sm_count()) * (k8 ? MA_PER_SM8 : MA_PER_SM32);
@@ -1277,7 +1277,7 @@ int launch_multi_adamw(MultiAdamWParams a, const GradPtrs& gp, int64_t blocks, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, multi_adamw_kernel<k8, G>, a, gp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, multi_adamw_kernel<k8, kStochastic, G>, a, gp) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1344,6 +1344,8 @@ int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t sta
     return QLORA_ERR_SHAPE;
   if (state->bits != 8 && state->bits != 32) return QLORA_ERR_UNSUPPORTED;
   if (grad_dtype != QLORA_DTYPE_F32 && grad_dtype != QLORA_DTYPE_BF16) return QLORA_ERR_UNSUPPORTED;
+  if (state->rounding != QLORA_ROUND_NEAREST && (state->rounding != QLORA_ROUND_STOCHASTIC || state->bits != 8))
+    return QLORA_ERR_UNSUPPORTED;
   if (state->bits == 8 && (!state->m_scale || !state->v_scale)) return QLORA_ERR_NULL;
   if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f && hp->eps > 0.0f &&
         hp->lr >= 0.0f && hp->weight_decay >= 0.0f && std::isfinite(hp->max_grad_norm)))
@@ -1395,9 +1397,14 @@ int qlora_multi_adamw_step(void* plan, size_t plan_bytes, int count, int64_t sta
   }
   const int64_t blocks = state_elems / MA_BLOCK;
   const bool f32 = grad_dtype == QLORA_DTYPE_F32;
-  if (state->bits == 8)
-    return f32 ? launch_multi_adamw<true, float>(a, gp, blocks, st) : launch_multi_adamw<true, uint16_t>(a, gp, blocks, st);
-  return f32 ? launch_multi_adamw<false, float>(a, gp, blocks, st) : launch_multi_adamw<false, uint16_t>(a, gp, blocks, st);
+  if (state->bits == 32)
+    return f32 ? launch_multi_adamw<false, false, float>(a, gp, blocks, st)
+               : launch_multi_adamw<false, false, uint16_t>(a, gp, blocks, st);
+  if (state->rounding == QLORA_ROUND_STOCHASTIC)
+    return f32 ? launch_multi_adamw<true, true, float>(a, gp, blocks, st)
+               : launch_multi_adamw<true, true, uint16_t>(a, gp, blocks, st);
+  return f32 ? launch_multi_adamw<true, false, float>(a, gp, blocks, st)
+             : launch_multi_adamw<true, false, uint16_t>(a, gp, blocks, st);
 }
 
 int qlora_merge_bf16(const qlora_nf4_t* Wq, const void* L1, const void* L2, int r, float s, void* out,

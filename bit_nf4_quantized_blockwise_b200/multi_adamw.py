@@ -20,6 +20,7 @@ from ._lib import (QLORA_DTYPE_BF16, QLORA_DTYPE_F32, _call, _check, _stream, li
 from .paged import AdamWConfig, ManagedBuffer, PagingPolicy
 
 STATE_BLOCK = 256
+ROUNDINGS = {"nearest": 0, "stochastic": 1}
 
 _dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 _device, _contiguous, _data_ptr = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
@@ -33,8 +34,11 @@ class MultiAdamW:
     copies (optional): one bf16 tensor per parameter, or None, written with the
     rounded parameter after each step (the factors the layer reads).
     state_bits: 32, or 8 (E4M3 codes of m and of sqrt(v) with one fp32 scale per
-    256 elements; include/qlora.h has the rule).  paged: state in unified
-    memory, moved by the policy of PagedAdamW.
+    256 elements; include/qlora.h has the rule).  rounding of the 8-bit codes:
+    "nearest", or "stochastic" (reproducible), which training over more than some
+    hundred steps needs: nearest codes do not follow the slow average of v where
+    the gradients' scale changes.  paged: state in unified memory, moved by the
+    policy of PagedAdamW.
 
     State, flat over all tensors: ``m`` and ``v`` (fp32, or float8_e4m3fn codes;
     in 8 bits ``v`` holds sqrt(v)), ``m_scale`` and ``v_scale`` (8 bits only)
@@ -44,11 +48,14 @@ class MultiAdamW:
 
     def __init__(self, params: Sequence[torch.Tensor], cfg: AdamWConfig = AdamWConfig(),
                  copies: Optional[Sequence[Optional[torch.Tensor]]] = None, state_bits: int = 32, paged: bool = False,
-                 watermark_bytes: int = 0, mem_info: Optional[Callable[[], Tuple[int, int]]] = None):
+                 watermark_bytes: int = 0, mem_info: Optional[Callable[[], Tuple[int, int]]] = None,
+                 rounding: str = "nearest"):
         self.params: List[torch.Tensor] = list(params)
         self.copies = [None] * len(self.params) if copies is None else list(copies)
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
+        if rounding not in ROUNDINGS or (rounding != "nearest" and state_bits != 8):
+            raise ValueError(f"rounding must be one of {sorted(ROUNDINGS)}, and 'nearest' with 32-bit state")
         if not self.params:
             raise ValueError("params is empty")
         if len(self.copies) != len(self.params):
@@ -66,7 +73,7 @@ class MultiAdamW:
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("params and copies overlap in memory")
-        self.cfg, self.state_bits = cfg, state_bits
+        self.cfg, self.state_bits, self.rounding = cfg, state_bits, rounding
         self.device = self.params[0].device
         self._numel = [p.numel() for p in self.params]
         self._shapes = [p.shape for p in self.params]
@@ -113,7 +120,7 @@ class MultiAdamW:
         st.m, st.v = self.m.data_ptr(), self.v.data_ptr()
         if self.state_bits == 8:
             st.m_scale, st.v_scale = self.m_scale.data_ptr(), self.v_scale.data_ptr()
-        st.steps, st.bits = self.steps.data_ptr(), self.state_bits
+        st.steps, st.bits, st.rounding = self.steps.data_ptr(), self.state_bits, ROUNDINGS[self.rounding]
         self._struct = st
 
     def _move(self, to_host: bool) -> None:
