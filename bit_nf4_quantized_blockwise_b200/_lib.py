@@ -602,9 +602,10 @@ def _workspace(ws: Optional[torch.Tensor], size: int, dev: torch.device) -> torc
 
 
 @functools.lru_cache(maxsize=4096)
-def _multi_ws_size(bwd: bool, *sizes: int) -> int:
+def _multi_ws_size(bwd: bool, device: int, *sizes: int) -> int:
     L = lib()
-    return (L.qlora_multi_linear_bwd_workspace_size if bwd else L.qlora_multi_linear_fwd_workspace_size)(*sizes)
+    with torch.cuda.device(device):  # the layout goes by the device's number of SMs
+        return (L.qlora_multi_linear_bwd_workspace_size if bwd else L.qlora_multi_linear_fwd_workspace_size)(*sizes)
 
 
 def _or_null(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -625,7 +626,7 @@ def qlora_multi_linear_fwd(Wq: NF4Weight, X: torch.Tensor, bank: AdapterBank, pl
     if T_save is None and save_T:
         T_save = torch.empty(M, r, dtype=torch.float32, device=dev)
     L = lib()
-    ws = _workspace(ws, _multi_ws_size(False, Wq.o, Wq.h, M, n, r), dev)
+    ws = _workspace(ws, _multi_ws_size(False, dev.index, Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_fwd, "qlora_multi_linear_fwd", dev, Wq.struct(), X.data_ptr(), M, bank.struct(),
           plan.buffer.data_ptr(), plan.buffer.numel(), Y.data_ptr(), _dtype_code(Y.dtype), _or_null(T_save),
           ws.data_ptr(), ws.numel() * ws.element_size())
@@ -648,7 +649,7 @@ def qlora_multi_linear_bwd(Wq: NF4Weight, X: torch.Tensor, dY: torch.Tensor, ban
     if dL2 is None:
         dL2 = torch.empty(n, r, Wq.o, dtype=torch.float32, device=dev)
     L = lib()
-    ws = _workspace(ws, _multi_ws_size(True, Wq.o, Wq.h, M, n, r), dev)
+    ws = _workspace(ws, _multi_ws_size(True, dev.index, Wq.o, Wq.h, M, n, r), dev)
     _call(L.qlora_multi_linear_bwd, "qlora_multi_linear_bwd", dev, Wq.struct(), X.data_ptr(), dY.data_ptr(), M,
           bank.struct(), plan.buffer.data_ptr(), plan.buffer.numel(), _or_null(T_saved), dX.data_ptr(),
           _dtype_code(dX.dtype), dL1.data_ptr(), dL2.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())

@@ -282,7 +282,8 @@ int qlora_adapter_plan(const int32_t* adapter, int64_t M, int n, void* plan, siz
  * gradients (dL1, dL2 are written in full).  M, X, dY, Y, dX, T_save, T_saved
  * and the weight as in qlora_linear_fwd / qlora_linear_bwd; plan: of the same M
  * and n, complete on `stream`; ws: device workspace of
- * qlora_multi_linear_*_workspace_size() bytes (0: sizes the layer does not take).
+ * qlora_multi_linear_*_workspace_size() bytes, asked with the call's device current (0:
+ * sizes the layer does not take).
  * W' is bf16; products are bf16 x bf16 accumulated in fp32.  T and U stay in
  * fp32 and enter the W' product as bf16 parts: two (16 bits) for a bf16 result,
  * three (24 bits) for an fp32 one and for the gradients.  Sums are added in a fixed order and results repeat bit for
