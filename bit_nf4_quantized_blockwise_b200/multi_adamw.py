@@ -183,7 +183,8 @@ class MultiAdamW:
         for x, scale in ((self.m, self.m_scale), (self.v, self.v_scale)):
             y = x[a:a + n].float()
             if scale is not None:
-                y = y * scale[a // STATE_BLOCK:].repeat_interleave(STATE_BLOCK)[:n]
+                first = a // STATE_BLOCK
+                y = y * scale[first:first - (-n // STATE_BLOCK)].repeat_interleave(STATE_BLOCK)[:n]
             out.append(y.view(self._shapes[i]))
         return out[0], out[1] if self.state_bits == 32 else out[1].square()
 

@@ -42,3 +42,43 @@ def test_workspace_sizes_are_those_of_the_call_s_device(monkeypatch):
         assert fake.queries == 6 and fake.current == 0
     finally:
         _lib._multi_ws_size.cache_clear()
+
+
+def _state_of(sizes):
+    """A MultiAdamW with 8-bit state on the CPU, not made by its constructor."""
+    from bit_nf4_quantized_blockwise_b200.multi_adamw import STATE_BLOCK, MultiAdamW
+    opt = MultiAdamW.__new__(MultiAdamW)
+    opt.state_bits, opt._numel, opt._shapes, opt.offsets, total = 8, list(sizes), [(n,) for n in sizes], [], 0
+    for n in sizes:
+        opt.offsets.append(total)
+        total += -(-n // STATE_BLOCK) * STATE_BLOCK
+    g = torch.Generator().manual_seed(0)
+    opt.m, opt.v = (torch.randn(total, generator=g).abs().to(torch.float8_e4m3fn) for _ in range(2))
+    opt.m_scale, opt.v_scale = (torch.rand(total // STATE_BLOCK, generator=g) for _ in range(2))
+    return opt
+
+
+@pytest.mark.parametrize("sizes", [(1,), (256,), (5, 700, 256, 257), (1000, 1)])
+def test_moments_decode_their_own_blocks(sizes):
+    opt = _state_of(sizes)
+    m = opt.m.float() * opt.m_scale.repeat_interleave(256)
+    v = (opt.v.float() * opt.v_scale.repeat_interleave(256)).square()
+    for i, n in enumerate(sizes):
+        a = opt.offsets[i]
+        got = opt.moments(i)
+        assert torch.equal(got[0], m[a:a + n]) and torch.equal(got[1], v[a:a + n])
+
+
+def test_moments_of_a_small_tensor_touch_nothing_else(monkeypatch):
+    """The scales of the tensors behind it are not expanded (of a large model, 4 bytes a parameter)."""
+    opt = _state_of((10, 1 << 20))
+    sizes = []
+    repeat = torch.Tensor.repeat_interleave
+
+    def counted(self, *args, **kw):
+        out = repeat(self, *args, **kw)
+        sizes.append(out.numel())
+        return out
+    monkeypatch.setattr(torch.Tensor, "repeat_interleave", counted)
+    opt.moments(0)
+    assert sizes and max(sizes) <= 256
