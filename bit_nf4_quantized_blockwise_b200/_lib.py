@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
@@ -246,7 +247,14 @@ def _check_linear(Wq: "NF4Weight", X, L1, L2, Y=None, T=None, dY=None, dX=None, 
 
 
 @functools.lru_cache(maxsize=64)
-def _codebook_of(codebook: Tuple[float, ...]):
+def _codebook_kept(codebook: Tuple[float, ...], zero_sign: float):
+    return _codebook_array(codebook)
+
+
+def _codebook_of(codebook):
+    """The C array of a codebook, kept for tuples of floats (0.0 and -0.0, which are equal, told apart)."""
+    if type(codebook) is tuple and codebook and type(codebook[0]) is float and 0.0 in codebook:
+        return _codebook_kept(codebook, math.copysign(1.0, codebook[codebook.index(0.0)]))
     return _codebook_array(codebook)
 
 
@@ -296,8 +304,8 @@ class NF4Weight:
         fp8, scale, mean, absmax, codebook = self.absmax_fp8, self.dq_scale, self.dq_mean, self.absmax, self.codebook
         return qlora_nf4_t(self.codes.data_ptr(), None if fp8 is None else fp8.data_ptr(),
                            None if scale is None else scale.data_ptr(), None if mean is None else mean.data_ptr(),
-                           self.o, self.h, _codebook_of(codebook) if type(codebook) is tuple else
-                           _codebook_array(codebook), 64, 256, None if absmax is None else absmax.data_ptr())
+                           self.o, self.h, _codebook_of(codebook), 64, 256,
+                           None if absmax is None else absmax.data_ptr())
 
 
 # ---------------------------------------------------------------- entry points
