@@ -30,7 +30,8 @@ class MultiAdamW:
     """AdamW over a list of fp32 CUDA tensors, updated in place.
 
     params: contiguous fp32 tensors of one device, none of them empty and no two
-    of them overlapping; their memory is used until the optimizer is dropped;
+    of them overlapping; their memory is used until the optimizer is dropped
+    (a step after one of them moved, as by x.data = y, is refused);
     copies (optional): one bf16 tensor per parameter, or None, written with the
     rounded parameter after each step (the factors the layer reads).
     state_bits: 32, or 8 (E4M3 codes of m and of sqrt(v) with one fp32 scale per
@@ -106,6 +107,7 @@ class MultiAdamW:
 
     def _make_plan(self) -> None:
         n = len(self.params)
+        self._places = self._addresses()
         table = (qlora_adamw_tensor_t * n)()
         for e, p, c in zip(table, self.params, self.copies):
             e.param, e.copy, e.n = p.data_ptr(), None if c is None else c.data_ptr(), p.numel()
@@ -122,6 +124,9 @@ class MultiAdamW:
             st.m_scale, st.v_scale = self.m_scale.data_ptr(), self.v_scale.data_ptr()
         st.steps, st.bits, st.rounding = self.steps.data_ptr(), self.state_bits, ROUNDINGS[self.rounding]
         self._struct = st
+
+    def _addresses(self) -> List[int]:
+        return list(map(_data_ptr, self.params)) + [c.data_ptr() for c in self.copies if c is not None]
 
     def _move(self, to_host: bool) -> None:
         for b in self._buffers:
@@ -145,6 +150,8 @@ class MultiAdamW:
         grads = list(grads)
         if len(grads) != len(self._numel):
             raise ValueError(f"{len(grads)} grads for {len(self._numel)} params")
+        if self._addresses() != self._places:
+            raise ValueError("params or copies have moved since the optimizer was made")
         at = [i for i, g in enumerate(grads) if g is not None]
         if not at:
             return

@@ -82,3 +82,17 @@ def test_moments_of_a_small_tensor_touch_nothing_else(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "repeat_interleave", counted)
     opt.moments(0)
     assert sizes and max(sizes) <= 256
+
+
+@pytest.mark.parametrize("which", ["params", "copies"])
+def test_a_step_refuses_tensors_that_have_moved(which):
+    """The plan holds the addresses of params and copies: a step after x.data = y would write to memory
+    that x no longer owns."""
+    opt = _state_of((5, 300))
+    opt.params = [torch.zeros(5), torch.zeros(300)]
+    opt.copies = [None, torch.zeros(300, dtype=torch.bfloat16)]
+    opt._places = opt._addresses()
+    tensor = getattr(opt, which)[1]
+    tensor.data = tensor.data.clone()
+    with pytest.raises(ValueError, match="moved"):
+        opt.step([torch.zeros(5), torch.zeros(300)])
