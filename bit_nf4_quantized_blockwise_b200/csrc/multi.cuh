@@ -1377,7 +1377,7 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(const __grid_constant
 // 13824, with it, and takes 167 and 1023 us so.
 // When the tiles are fewer than the SMs a group's blocks are dealt to `split`
 // items, whose sums go to the partial buffer and are added in order by the one
-// that ends last.  No sum depends on timing; adapters without tokens get zeros.
+// that ends last (each epilogue warp its own rows).  No sum depends on timing; adapters without tokens get zeros.
 constexpr int MD_BM = 128;
 constexpr int MD_BN = 64;
 constexpr int MD_BK = 64;
@@ -1405,7 +1405,7 @@ struct MultiGradParams {
   int tiles;           // and of dL2
   int split;           // parts of a group's blocks
   float* partial;      // [group][tile][part] sums of [64][128]
-  unsigned* counters;  // [group][tile], zero at launch
+  unsigned* counters;  // [group][tile][epilogue warp], zero at launch
 };
 
 // Replaces what is not finite among the `ranks` elements (a multiple of 8) of row m of a factor's
@@ -1617,14 +1617,13 @@ __global__ void __launch_bounds__(MD_THREADS, 1)
         float* part = p.partial + (tile_index * p.split + it.part) * (MD_BM * MD_BN) + row;  // [rank][row]: coalesced
 #pragma unroll
         for (int j = 0; j < MD_BN; ++j) part[j * MD_BM] = x[j];
+        // by warp, each for its own 32 rows: a barrier of the four would wait for good where one gave up
         __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the epilogue warps
-        __shared__ unsigned order;
-        if (threadIdx.x == 64) order = atomicAdd(&p.counters[tile_index], 1u);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const bool last = order == static_cast<unsigned>(p.split - 1);
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // order has been read by all
-        if (!last) continue;
+        __syncwarp();
+        unsigned prior = 0;
+        if (lane == 0) prior = atomicAdd(&p.counters[tile_index * 4 + q], 1u);
+        prior = __shfl_sync(0xFFFFFFFFu, prior, 0);
+        if (prior != static_cast<unsigned>(p.split - 1)) continue;
         __threadfence();
         const float* first = p.partial + tile_index * p.split * (MD_BM * MD_BN) + row;
 #pragma unroll

@@ -1628,8 +1628,8 @@ MultiWs multi_ws_layout(void* base, int64_t o, int64_t h, int64_t M, int n, int 
     const int64_t items = grad_tiles(o, h, r) * (n < M ? n : M), split = grad_split(M, n, grad_tiles(o, h, r));
     if (split > 1) {
       w.Gpart = static_cast<float*>(take(items * split * MD_BM * MD_BN * 4));
-      w.n_gcnt = static_cast<int>(items);
-      w.Gcnt = static_cast<unsigned*>(take(items * 4));
+      w.n_gcnt = static_cast<int>(items * 4);
+      w.Gcnt = static_cast<unsigned*>(take(items * 4 * 4));
     }
   }
   w.bytes = off;
