@@ -1395,8 +1395,8 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
 
 // NG token groups of 8 (NG = 1: M <= 8, NG = 2: M <= 16).  kLora = false
 // (tokens with different adapters) only sums T for the kernel that adds the
-// adapters' term.
-template <int NG, bool kLora>
+// adapters' term.  kSeg: the sums are flushed inside a tile too.
+template <int NG, bool kLora, bool kSeg = false>
 __global__ void __launch_bounds__(SD_THREADS, 1)
     small_m_mma_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                        const __grid_constant__ DecodeParams p) {
@@ -1540,13 +1540,21 @@ __global__ void __launch_bounds__(SD_THREADS, 1)
     };
 #pragma unroll
     for (int i = 0; i < kPre; ++i) fetch(uc[i]);
-    float acc[2][NG][4];
+    // The tensor core cuts its running sum at every step of 16 products.  Without the LoRA term an fp32
+    // result is to be as exact as an fp32 sum: up to 8 tokens the accumulators are added to others in
+    // registers after every kPre units (512 products; error 3e-7 at K = 8192 for 12e-7); above, where there
+    // are no registers for that (16 tokens, 8192 x 22016: 84 us a call for 75), they are flushed after 1024
+    // products (kSeg; 79 us, 7e-7), for fp32 results alone.
+    constexpr bool kSums = !kLora && NG == 1;
+    constexpr int kSegUnits = 4 * SD_GROUPS;
+    bool begun = false;
+    float acc[2][NG][4], sum[2][NG][4];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
       for (int q = 0; q < NG; ++q)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[rt][q][v] = 0.0f;
+        for (int v = 0; v < 4; ++v) acc[rt][q][v] = sum[rt][q][v] = 0.0f;
     int acc_tile = cur.tile;
     auto flush = [&]() {
       pdl_wait();  // the output was zeroed by the rank-r kernel
@@ -1560,8 +1568,10 @@ __global__ void __launch_bounds__(SD_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int m = 8 * q + 2 * t + c;
-              if (n < p.N && m < p.M) atomicAdd(p.out + static_cast<int64_t>(m) * p.N + n, acc[rt][q][2 * hh + c]);
-              acc[rt][q][2 * hh + c] = 0.0f;
+              float& x = acc[rt][q][2 * hh + c];
+              float& y = sum[rt][q][2 * hh + c];
+              if (n < p.N && m < p.M) atomicAdd(p.out + static_cast<int64_t>(m) * p.N + n, kSums ? y + x : x);
+              x = y = 0.0f;
             }
           }
         }
@@ -1575,10 +1585,13 @@ __global__ void __launch_bounds__(SD_THREADS, 1)
           ok = false;
           break;
         }
-        if (cur.tile != acc_tile) {
+        // a group's units are SD_GROUPS apart: its first one of a segment
+        const bool seg = kSeg && begun && cur.k % kSegUnits < SD_GROUPS;
+        if (cur.tile != acc_tile || seg) {
           flush();
           acc_tile = cur.tile;
         }
+        begun = true;
         const int cs = cur.cr.slot;
         const UnitConst un = uc[it];
         const int nb = min(SD_UNIT_BLOCKS, p.blocks_per_row - cur.k * SD_UNIT_BLOCKS);
@@ -1666,6 +1679,17 @@ __global__ void __launch_bounds__(SD_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[cs]);
         cur.step(SD_GROUPS);
+      }
+      if constexpr (kSums) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+          for (int q = 0; q < NG; ++q)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              sum[rt][q][v] += acc[rt][q][v];
+              acc[rt][q][v] = 0.0f;
+            }
       }
     }
     flush();

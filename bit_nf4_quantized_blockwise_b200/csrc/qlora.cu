@@ -1834,10 +1834,18 @@ int launch_multi_decode(const qlora_nf4_t* Wq, const void* X, const qlora_adapte
     dp.absmax32 = Wq->absmax;
     dp.out = acc;
     std::memcpy(dp.codebook, Wq->codebook, sizeof(dp.codebook));
-    auto kernel = M <= 8 ? small_m_mma_kernel<1, false> : small_m_mma_kernel<2, false>;
-    if ((M <= 8 ? set_smem_once<small_m_mma_kernel<1, false>>(SD_SMEM_BYTES)
-                : set_smem_once<small_m_mma_kernel<2, false>>(SD_SMEM_BYTES)) != QLORA_OK)
-      return QLORA_ERR_CUDA;
+    auto kernel = small_m_mma_kernel<1, false>;
+    int set = QLORA_OK;
+    if (M <= 8) {
+      set = set_smem_once<small_m_mma_kernel<1, false>>(SD_SMEM_BYTES);
+    } else if (y_dtype == QLORA_DTYPE_BF16) {
+      kernel = small_m_mma_kernel<2, false>;
+      set = set_smem_once<small_m_mma_kernel<2, false>>(SD_SMEM_BYTES);
+    } else {
+      kernel = small_m_mma_kernel<2, false, true>;
+      set = set_smem_once<small_m_mma_kernel<2, false, true>>(SD_SMEM_BYTES);
+    }
+    if (set != QLORA_OK) return QLORA_ERR_CUDA;
     LaunchScope ls(QLORA_KERNEL_SMALL_M, st);
     rc = launch_dependent(kernel, dim3(static_cast<unsigned>(dp.units < sm_count() ? dp.units : sm_count())), SD_THREADS,
                           SD_SMEM_BYTES, st, mc, mx, dp);

@@ -3,7 +3,7 @@ term, against 64 bits.
 
 u = 2^-24.  The tensor core cuts its running sum by up to a step of fp32, 2 u of it, at every 16
 products.  Above 32 tokens an accumulator ends after 1024 products (fp32 results: 512, and 256 where
-there are 2048 or fewer) and is added in fp32."""
+there are 2048 or fewer) and is added in fp32, up to 8 tokens after 512."""
 import numpy as np
 import pytest
 import torch
@@ -72,6 +72,16 @@ def test_fp32_results_are_as_exact_as_fp32_sums(k, steps, bwd):
     got, want = _base(w, x, bwd, torch.float32)
     off = float(((got.double() - want).abs() / want).max()) / U
     assert off <= steps + 1 + k // (16 * steps), off
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_decode_results_are_as_exact_as_fp32_sums(M):
+    """Up to 8 tokens accumulators of 512 products, 33 u S, up to 16 of 1024, 65 u S; they are added to sums
+    in registers, 4 at most for K = 8192 and a warp, or to the result, fewer than 12 for all warps: 16 u S
+    at most.  (In accumulators of 2048 products the cut may be 129 u.)"""
+    w, x = _all_positive(M, 74 * 256, 8192, 8192)
+    got, want = _base(w, x, False, torch.float32)
+    assert float(((got.double() - want).abs() / want).max()) / U <= (33 if M <= 8 else 65) + 16
 
 
 @pytest.mark.parametrize("bwd", [False, True])
