@@ -214,6 +214,8 @@ class MultiAdamW:
             steps = state["steps"]
         if isinstance(steps, torch.Tensor) and steps.shape != self.steps.shape:
             raise ValueError(f"steps must have {self.steps.numel()} entries")
+        if (int(steps.min()) if isinstance(steps, torch.Tensor) else int(steps)) < 0:
+            raise ValueError("steps holds a negative count")
         for k in want:
             getattr(self, k).copy_(state[k])
         if isinstance(steps, torch.Tensor):

@@ -96,3 +96,18 @@ def test_a_step_refuses_tensors_that_have_moved(which):
     tensor.data = tensor.data.clone()
     with pytest.raises(ValueError, match="moved"):
         opt.step([torch.zeros(5), torch.zeros(300)])
+
+
+@pytest.mark.parametrize("steps", [-1, torch.tensor([3, -2], dtype=torch.int32)])
+def test_loading_refuses_negative_step_counts(steps):
+    """The first step after -1 would divide by 1 - beta^0 = 0 and make every parameter NaN."""
+    opt = _state_of((5, 300))
+    opt.steps = torch.tensor([7, 8], dtype=torch.int32)
+    state = {k: getattr(opt, k).clone() for k in ("m", "v", "m_scale", "v_scale")}
+    before = opt.m.clone()
+    state["m"] = torch.zeros_like(before)
+    with pytest.raises(ValueError, match="negative"):
+        opt.load_state(state, steps=steps)
+    assert opt.steps.tolist() == [7, 8] and torch.equal(opt.m.view(torch.uint8), before.view(torch.uint8))
+    opt.load_state(state, steps=torch.tensor([0, 4], dtype=torch.int32))
+    assert opt.steps.tolist() == [0, 4]
