@@ -146,7 +146,10 @@ class MultiAdamW:
         """One step: grads[i] (fp32 or bf16, all the same type, shaped like
         params[i]) or None, which leaves parameter, state and step count i as
         they are.  The gradients are not modified.  May be captured into a CUDA
-        graph: the step counts live on the device."""
+        graph: the step counts live on the device.  A captured step keeps what the
+        call was given for good: the gradients' addresses, which of them are None,
+        and the numbers of cfg (learning rate, clipping bound and the others), so a
+        changed learning rate needs a new capture."""
         grads = list(grads)
         if len(grads) != len(self._numel):
             raise ValueError(f"{len(grads)} grads for {len(self._numel)} params")

@@ -392,6 +392,8 @@ int qlora_adamw_step(float* param, const float* grad, float* m, float* v, uint16
  *           grad_dtype says, element-aligned; NULL leaves the tensor, its state
  *           and its step count as they are.  Not modified.
  *   hp    : step is not used (see steps); max_grad_norm <= 0: no clipping.
+ *   A captured call keeps the addresses in grads and the numbers in hp, learning rate
+ *   and clipping bound among them: a change of theirs needs a new capture.
  *   A gradient with NaN or infinity: the norm clips nothing (NaN) or everything
  *   (infinity), as in qlora_adamw_step; its element becomes NaN.  With 8-bit
  *   state a NaN's m and r are NaN too, and an infinity makes m of its whole
