@@ -24,6 +24,10 @@
 // value itself times inf is not.  Every element that comes out non-finite is
 // therefore computed once more from its own row and adapter alone, in fp32 and
 // with whole values; a finite batch never gets there.
+//
+// Times in these comments are of calls in a loop over two or three sets of inputs at
+// the step that they describe, unless they say cold; a call with a cold L2 takes 2 to
+// 15 % longer.
 #pragma once
 
 #include "qlora.h"
@@ -985,10 +989,10 @@ constexpr int MG_PAIR_SMEM = PG_SMEM_BYTES + 16 + MG_PAIR_ITEMS * static_cast<in
 // `chain` stages of 128 products, and the epilogue, eight warps with 128 sums a
 // thread, adds it in registers while the MMAs go on with the other one.  (Running
 // sums in memory instead, 256 KB a pair in L2: 453 us for 345 at 4096 x 4096 x 11008.)
-//   bf16 results: 8 stages (0.07 % there).  One accumulator: 289 us a call of 4096 x
-//   4096 x 11008 with an L2 flushed before it, 16 stages 293, 8 stages 301, 4 stages 328.
+//   bf16 results: 8 stages (0.07 % there).  One accumulator: 289 us a cold call of 4096 x
+//   4096 x 11008, 16 stages 293, 8 stages 301, 4 stages 328.
 //   fp32 results: as exact as an fp32 sum.  4 stages, 3.4e-7 (fp32 sums of K = 4096:
-//   5.1e-7), 368 us for 344 with 8 stages (7.4e-7); up to K = 2048, where an fp32 sum
+//   5.1e-7), 368 us cold for 344 with 8 stages (7.4e-7); up to K = 2048, where an fp32 sum
 //   is better than that (1.6e-7 at 768) and the product a smaller part of the call, 2
 //   stages, 1.9e-7 (4096 x 4096 x 11008 would take 405 us).
 constexpr int multi_chain(bool out_bf16, int64_t K) { return out_bf16 ? 8 : (K > 2048 ? 4 : 2); }

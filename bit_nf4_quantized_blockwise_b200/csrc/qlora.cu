@@ -1992,7 +1992,7 @@ int qlora_multi_linear_fwd(const qlora_nf4_t* Wq, const void* X, int64_t M, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (M <= kMultiDecodeMax) return launch_multi_decode(Wq, X, ad, Y, y_dtype, T_save, w, v, st);
   // the rank-r product first: the dequantization, which needs nothing of it and whole SMs, then starts on
-  // each SM as that ends there (333 tokens, 13824 x 5120: 125 -> 121 us a call)
+  // each SM as that ends there (333 tokens, 13824 x 5120: 125 -> 121 us a call in a loop)
   const SortParams sort = sort_params(X, w.Xs, h, nullptr, nullptr, 0);
   rc = launch_shrink<true>(X, ad->L1, h, r, w.PT, v, true, st, nullptr, 0, &sort);
   if (rc == QLORA_OK) rc = dequant_into(Wq, w.Wd, QLORA_KERNEL_WPRIME, st, true);
