@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(MS_THREADS, RP <= 64 ? 3 : 2)
 
 // Fills the slots of T (or U): the sum of the K parts in order, or a T given by
 // the caller, times the adapter's scale, as `parts` bf16 terms: two keep 16 bits
-// of the value, which is 256 steps of a bf16 result; three keep 24, for fp32
+// of the value, 256 times finer than a bf16 result; three keep 24, for fp32
 // results (those of the W' product, and the sums over tokens).  Also writes T itself in the
 // batch's order, zero for tokens without adapter.  blockIdx.x < max_slots: 64
 // rows (blockIdx.y) of a slot; above: the rows without adapter of a tile.
